@@ -4,9 +4,9 @@ Three families: the router (logits to the expert ids and gates that the layer ta
 the MXFP4 quantisation of expert weights, and the expert FFN on MXFP4 weights.  ``run`` computes them in
 their plain form from elementary torch operations, or, where ``own`` is true, with the library's calls.
 
-MXFP4 and MXFP8 here: blocks of 32 consecutive values along the contraction axis share a power of two,
-2^(floor(log2(largest magnitude)) - 2) for e2m1 elements and ... - 8 for e4m3 elements; each element is
-the value divided by it, rounded to nearest, ties to even, saturated at 6 and 448.
+MXFP4 and MXFP6 here: blocks of 32 consecutive values along the contraction axis share a power of two,
+2^(floor(log2(largest magnitude)) - 2); each element is the value divided by it, as an e2m1 (MXFP4) or
+e2m3 (MXFP6) number: rounded to nearest, ties to even, saturated at 6 and 7.5.
 """
 
 import math
@@ -55,9 +55,9 @@ def listed():
         # one token through the decode workload's experts
         dict(_ffn(1, 7168, 2048, 32, 8, "mxfp4"), name="ffn token"),
         # the decode workload, with the finer activations
-        dict(_ffn(128, 7168, 2048, 32, 8, "mxfp8"), name="ffn decode"),
+        dict(_ffn(128, 7168, 2048, 32, 8, "mxfp6"), name="ffn decode"),
         # sizes that are no multiple of any tile
-        dict(_ffn(601, 264, 200, 6, 2, "mxfp8"), name="ffn ragged"),
+        dict(_ffn(601, 264, 200, 6, 2, "mxfp6"), name="ffn ragged"),
         # the prefill workload
         dict(_ffn(4096, 2048, 1408, 64, 6, "mxfp4"), name="ffn prefill"),
         # the skewed workload: popular experts with thousands of rows, others empty
@@ -86,7 +86,7 @@ def draw(rng):
                          rng.choice([1, 2]), dtype)
     E = _log(rng, 2, 64)
     return _ffn(_log(rng, 1, 4096), 8 * _log(rng, 16, 512), 8 * _log(rng, 16, 256), E,
-                rng.randint(1, min(8, E)), rng.choice(["mxfp4", "mxfp8"]),
+                rng.randint(1, min(8, E)), rng.choice(["mxfp4", "mxfp6"]),
                 rng.choice(["uniform", "zipf"]))
 
 
@@ -116,11 +116,10 @@ def _round_e2m1(a):
     return (torch.round(a / step) * step).clamp(max=6.0)
 
 
-def _round_e4m3(a):
-    """Magnitudes to the nearest with three fraction bits, down to steps of 2^-9 (ties to even)."""
-    e = (torch.frexp(a)[1] - 1).clamp(min=-6)
-    step = ((e - 3 + 127) << 23).view(torch.float32)
-    return (torch.round(a / step) * step).clamp(max=448.0)
+def _round_e2m3(a):
+    """Magnitudes to the nearest in steps of 1/8 up to 2, 1/4 up to 4, 1/2 up to 7.5."""
+    step = torch.where(a < 2, 0.125, torch.where(a < 4, 0.25, 0.5))
+    return (torch.round(a / step) * step).clamp(max=7.5)
 
 
 def _mx(v, fmt="mxfp4"):
@@ -128,11 +127,11 @@ def _mx(v, fmt="mxfp4"):
     n = v.shape[-1]
     v = torch.nn.functional.pad(v, (0, -n % 32)).unflatten(-1, (-1, 32))
     top = v.abs().amax(-1, keepdim=True)
-    e = torch.frexp(top)[1] - 1 - (2 if fmt == "mxfp4" else 8)
+    e = torch.frexp(top)[1] - 1 - 2
     e = torch.where(top > 0, e, 0).clamp(min=-125)
     unit, inverse = (((s * e + 127) << 23).view(torch.float32) for s in (1, -1))
     a = v.abs() * inverse
-    q = (_round_e2m1(a) if fmt == "mxfp4" else _round_e4m3(a)) * unit
+    q = (_round_e2m1(a) if fmt == "mxfp4" else _round_e2m3(a)) * unit
     return torch.copysign(q, v).flatten(-2)[..., :n]
 
 
@@ -317,9 +316,7 @@ def run(state):
 def _grid(fmt):
     if fmt == "mxfp4":
         return [0, 0.5, 1, 1.5, 2, 3, 4, 6]
-    sub = [m * 2.0 ** -9 for m in range(8)]
-    normal = [(1 + m / 8) * 2.0 ** e for e in range(-6, 9) for m in range(8)]
-    return [v for v in sub + normal if v <= 448]
+    return [m / 8 for m in range(16)] + [2 + m / 4 for m in range(8)] + [4 + m / 2 for m in range(8)]
 
 
 def _mx64(v, fmt):
@@ -330,7 +327,7 @@ def _mx64(v, fmt):
     exponent = torch.floor(torch.log2(torch.where(top > 0, top, 1.0)))
     # log2 next to a power of two may round up to it
     exponent = torch.where(torch.exp2(exponent) > top, exponent - 1, exponent)
-    unit = torch.exp2(torch.where(top > 0, exponent, 0.0) - (2 if fmt == "mxfp4" else 8))
+    unit = torch.exp2(torch.where(top > 0, exponent, 0.0) - 2)
     grid = torch.tensor(_grid(fmt), dtype=torch.float64, device=v.device)
     a = v.abs() / unit
     middle = (grid[1:] + grid[:-1]) / 2
