@@ -374,6 +374,106 @@ int moe_ffn_bwd_w(const moe_ffn_problem *p, const void *dy, const void *x, const
                   void *d_up_proj_weight, void *d_down_proj_weight, void *ws, size_t ws_bytes,
                   uint32_t flags, void *stream);
 
+/* ---- router ----------------------------------------------------------------- */
+
+/* Where topk_ids and topk_weights come from (the layer's inputs, HyperMegaMoE
+ * issue page, section 3.1): for router logits l [T, E] with scores
+ * s = softmax(l) over the E experts or sigmoid(l),
+ *
+ *     key_j = s_j + bias_j         (selection only; no bias: the scores' order)
+ *     topk_ids     = the K experts of largest key, descending, ties to the lower id
+ *     topk_weights = scale · s_id, divided by the sum of the K selected scores
+ *                    if `renormalize`
+ *
+ * `groups` > 1 with topk_groups < groups first keeps the topk_groups groups
+ * (of E / groups consecutive experts) with the largest value, the value being
+ * the group's largest key (group_top 1) or the sum of its two largest
+ * (group_top 2), ties to the lower group.  Scores that are added up before
+ * they are compared are formed and compared in 64 bits.
+ *
+ * An expert whose logit or bias is -inf is closed to that token.  A slot left
+ * without an open expert (a padded token's row of -inf, say) gets id -1 and
+ * gate 0: moe_ffn_fwd drops such a slot (and records MOE_FFN_DEV_BAD_ID).  A
+ * NaN key is below every number; under softmax a NaN or +inf logit makes all
+ * gates of its row NaN.
+ *
+ * Limits: those of moe_ffn_problem for T, K and E; K <= E and at most the
+ * topk_groups · E / groups experts of the kept groups; groups <= 64 divides E;
+ * group_top 2 needs two experts a group. */
+typedef enum { MOE_FFN_SCORE_SOFTMAX = 0, MOE_FFN_SCORE_SIGMOID = 1 } moe_ffn_score;
+typedef struct {
+    int64_t T, E, K;
+    int64_t logits_stride; /* elements from one token's logits to the next, >= E */
+    int32_t logits_dtype;  /* MOE_FFN_F32 or MOE_FFN_BF16 */
+    int32_t ids_dtype;     /* MOE_FFN_I32 or MOE_FFN_I64 */
+    int32_t score;         /* moe_ffn_score */
+    int32_t renormalize;   /* 0 or 1 */
+    int32_t groups, topk_groups, group_top; /* 1, 1, 1: no groups */
+    float scale;
+} moe_ffn_router;
+
+/* topk_ids [T, K] and topk_weights [T, K] (fp32) from logits (rows
+ * logits_stride apart; aligned to their element) and bias [E] fp32 or NULL.
+ * Needs no workspace and may be captured into a graph. */
+int moe_ffn_router_fwd(const moe_ffn_router *r, const void *logits, const float *bias,
+                       void *topk_ids, float *topk_weights, void *stream);
+/* d_logits [T, E] (dense rows, logits_dtype, overwritten) from d_topk_weights
+ * [T, K] fp32 (moe_ffn_bwd's output, say), the same logits and the ids the
+ * forward chose.  The selection is a constant: bias and groups have no
+ * gradient and are not read.  A slot whose id is outside [0, E) or whose
+ * expert is closed contributes nothing. */
+int moe_ffn_router_bwd(const moe_ffn_router *r, const float *d_topk_weights, const void *logits,
+                       const void *topk_ids, void *d_logits, void *stream);
+
+/* ---- expert FFN on MXFP4 weights ---------------------------------------------- */
+
+/* Inference with the expert weights in 4 bits.  MXFP4: blocks of 32
+ * consecutive values along the contraction axis share a power of two
+ * 2^(floor(log2 m) - 2), m the block's largest magnitude, and each value is
+ * kept as an e2m1 number (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives),
+ * rounded to nearest with ties to even and saturated: 17 bits for 4 values.
+ * MXFP6 is the same with e2m3 numbers (three fraction bits, up to 7.5).  A block
+ * with a NaN or an infinity becomes NaN.  (OCP microscaling formats 1.0.) */
+enum { MOE_FFN_MXFP4 = 4, MOE_FFN_MXFP6 = 5 }; /* activation formats */
+
+/* A stack of E weight matrices [Kd, N] (Kd the contraction length), row-major,
+ * in `dtype` (F32 or BF16).  `panels` equal column panels are laid out apart:
+ * 2 for up_proj_weight (gate and up), 1 for down_proj_weight.  Limits:
+ * 1 <= E <= 1024, Kd % 8 == 0, N % (8 · panels) == 0, panels 1 or 2,
+ * Kd · N < 2^31. */
+typedef struct {
+    int64_t E, Kd, N;
+    int32_t panels;
+    int32_t dtype;
+} moe_ffn_mxfp4_weight;
+
+/* Bytes of the packed form, an opaque buffer for the calls below (pure host
+ * function). */
+int moe_ffn_mxfp4_weight_size(const moe_ffn_mxfp4_weight *w, size_t *packed_bytes);
+/* weight [E, Kd, N] -> packed (16-byte aligned, of packed_bytes at least). */
+int moe_ffn_mxfp4_quantize(const moe_ffn_mxfp4_weight *w, const void *weight, void *packed,
+                           size_t packed_bytes, void *stream);
+/* The values that `packed` stands for -> weight [E, Kd, N], exactly. */
+int moe_ffn_mxfp4_dequantize(const moe_ffn_mxfp4_weight *w, const void *packed,
+                             size_t packed_bytes, void *weight, void *stream);
+
+/* Workspace of moe_ffn_mxfp4_fwd.  Pure host function. */
+int moe_ffn_mxfp4_workspace_size(const moe_ffn_problem *p, int32_t act_format, uint32_t flags,
+                                 size_t *ws_bytes);
+/* moe_ffn_fwd (saved = NULL) on packed weights: up_packed of {E, H, 2I, 2
+ * panels}, down_packed of {E, I, H, 1 panel}.  The token rows, and
+ * act = silu(gate) ⊙ up, are quantised to act_format (MOE_FFN_MXFP4 or
+ * MOE_FFN_MXFP6) in blocks of 32 along H and I before their product; sums are
+ * fp32; an expert's output row is rounded to bf16 before the combine, as in
+ * moe_ffn_fwd.  A NaN or infinity in a token's row makes that token's
+ * output NaN and no other's.  dtype must be BF16 and Is 0; the flags
+ * MOE_FFN_CHECK_IDS and MOE_FFN_CHECK_STATUS apply, others are rejected with
+ * MOE_FFN_ERR_SHAPE. */
+int moe_ffn_mxfp4_fwd(const moe_ffn_problem *p, int32_t act_format, const void *x,
+                      const void *topk_ids, const float *topk_weights, const void *up_packed,
+                      const void *down_packed, void *y, void *ws, size_t ws_bytes, uint32_t flags,
+                      void *stream);
+
 /* ---- status and measurement helpers ---------------------------------------- */
 
 /* Synchronises `stream`, then reads the device status word that the last

@@ -12,6 +12,11 @@ Public API (names follow the C ABI of ``include/moe_ffn.h``):
   save_for_backward=False, check_ids=False)`` -> ``y`` (and the saved context)
 * ``moe_ffn_route(topk_ids, E)`` -> counts, offsets, sorted_slot, slot_pos
 * ``moe_ffn(...)`` autograd-aware layer (forward + backward through the library)
+* ``moe_ffn_router(logits, K, ...)`` autograd-aware router -> topk_weights, topk_ids
+  (``moe_ffn_router_fwd`` and ``moe_ffn_router_bwd`` are its two halves)
+* ``moe_ffn_mxfp4_quantize(weight, panels)`` -> packed 4-bit expert weights
+  (``moe_ffn_mxfp4_dequantize`` gives the values back)
+* ``moe_ffn_mxfp4_fwd(x, topk_ids, topk_weights, up, down, act="mxfp4")`` -> ``y``
 """
 
 from __future__ import annotations
@@ -47,6 +52,16 @@ __all__ = [
     "moe_ffn_bwd",
     "moe_ffn",
     "MoEFFNFunction",
+    "Router",
+    "moe_ffn_router_fwd",
+    "moe_ffn_router_bwd",
+    "moe_ffn_router",
+    "MoERouterFunction",
+    "MXFP4Weight",
+    "moe_ffn_mxfp4_quantize",
+    "moe_ffn_mxfp4_dequantize",
+    "mxfp4_workspace_size",
+    "moe_ffn_mxfp4_fwd",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -65,6 +80,8 @@ TEST_DROP_RELEASE = 0x100
 TEST_SMALL_GRID = 0x200
 CHECK_SAVED = 0x4
 DEV_BAD_ID, DEV_TIMEOUT, DEV_BAD_SAVED, DEV_BAD_WS = 0x1, 0x2, 0x4, 0x8
+SCORES = {"softmax": 0, "sigmoid": 1}
+ACT_FORMATS = {"mxfp4": 4, "mxfp6": 5}
 STAGES = ("route", "gemm1", "gemm2", "combine", "pipeline")
 BWD_STAGES = ("act_grad", "input_grad", "dx_combine", "w2_grad", "w1_grad")
 
@@ -91,6 +108,20 @@ class SharedWeights(ctypes.Structure):
 
 class SharedGrads(ctypes.Structure):
     _fields_ = [("d_up_proj_weight", ctypes.c_void_p), ("d_down_proj_weight", ctypes.c_void_p)]
+
+
+class Router(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("logits_stride", ctypes.c_int64), ("logits_dtype", ctypes.c_int32),
+                ("ids_dtype", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class MXFP4Stack(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int64), ("Kd", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("panels", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 class FwdStageLayout(ctypes.Structure):
@@ -153,6 +184,13 @@ def load_library():
             "moe_ffn_route": [pp, vp, vp, vp, vp, vp, vp, sz, vp],
             "moe_ffn_fwd_noalloc": [pp, vp, vp, vp, vp, vp, vp, u32, vp],
             "moe_ffn_fwd_stages": [pp, u32, ctypes.POINTER(FwdStageLayout)],
+            "moe_ffn_router_fwd": [ctypes.POINTER(Router), vp, vp, vp, vp, vp],
+            "moe_ffn_router_bwd": [ctypes.POINTER(Router), vp, vp, vp, vp, vp],
+            "moe_ffn_mxfp4_weight_size": [ctypes.POINTER(MXFP4Stack), psz],
+            "moe_ffn_mxfp4_quantize": [ctypes.POINTER(MXFP4Stack), vp, vp, sz, vp],
+            "moe_ffn_mxfp4_dequantize": [ctypes.POINTER(MXFP4Stack), vp, sz, vp, vp],
+            "moe_ffn_mxfp4_workspace_size": [pp, i32, u32, psz],
+            "moe_ffn_mxfp4_fwd": [pp, i32, vp, vp, vp, vp, vp, vp, vp, sz, u32, vp],
             "moe_ffn_read_status": [vp, vp, ctypes.POINTER(ctypes.c_int32)],
             "moe_ffn_event_create": [ctypes.POINTER(ctypes.c_void_p)],
             "moe_ffn_event_destroy": [vp],
@@ -195,12 +233,16 @@ def _dtype_code(t: torch.Tensor) -> int:
     raise MoEFFNError(3, f"unsupported dtype {t.dtype}; use float32 or bfloat16")
 
 
-def _ids_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.int32:
+def _ids_code_of(dtype) -> int:
+    if dtype == torch.int32:
         return I32
-    if t.dtype == torch.int64:
+    if dtype == torch.int64:
         return I64
-    raise MoEFFNError(3, f"topk_ids must be int32 or int64, got {t.dtype}")
+    raise MoEFFNError(3, f"topk_ids must be int32 or int64, got {dtype}")
+
+
+def _ids_code(t: torch.Tensor) -> int:
+    return _ids_code_of(t.dtype)
 
 
 def _ptr(t):
@@ -529,6 +571,207 @@ def moe_ffn_route(topk_ids: torch.Tensor, E: int, H: int = 8, I: int = 8):
                                _stream(dev))
     _check(rc)
     return counts, offsets, sorted_slot[:T * K], slot_pos[:T * K], ws
+
+
+def _router(logits, K, ids_dtype, score, renormalize, groups, topk_groups, group_top, scale):
+    if not logits.is_cuda:
+        raise MoEFFNError(1, "all tensors must be on the GPU (no CPU fallback exists)")
+    if logits.dim() != 2:
+        raise MoEFFNError(2, "expected logits [T, E]")
+    if logits.stride(1) != 1 and logits.shape[1] > 1:
+        raise MoEFFNError(4, "a token's logits must be consecutive")
+    if score not in SCORES:
+        raise MoEFFNError(2, f"score must be one of {sorted(SCORES)}, got {score!r}")
+    T, E = logits.shape
+    stride = logits.stride(0) if T > 1 else max(E, 1)
+    return Router(T, E, K, stride, _dtype_code(logits), ids_dtype, SCORES[score],
+                  1 if renormalize else 0, groups, topk_groups, group_top, scale)
+
+
+def _same_device(t, *others):
+    for o in others:
+        if o is not None and o.device != t.device:
+            raise MoEFFNError(1, f"tensors on {t.device} and {o.device}: one device is needed")
+
+
+def moe_ffn_router_fwd(logits, K: int, *, bias=None, score: str = "softmax",
+                       renormalize: bool = True, groups: int = 1, topk_groups: int = 1,
+                       group_top: int = 1, scale: float = 1.0, ids_dtype=torch.int32):
+    """(topk_weights [T, K] fp32, topk_ids [T, K]) of router logits [T, E] (see
+    include/moe_ffn.h, moe_ffn_router_fwd).
+
+    ``logits`` are float32 or bfloat16; their rows may be strided.  ``bias`` [E]
+    float32 shifts the scores for the selection only.  With ``groups`` > 1 the
+    experts come from the ``topk_groups`` best groups.  A slot without an open
+    expert (every other logit -inf) has id -1 and weight 0.
+    """
+    lib = load_library()
+    ids_code = _ids_code_of(ids_dtype)
+    r = _router(logits, K, ids_code, score, renormalize, groups, topk_groups, group_top, scale)
+    if bias is not None:
+        _require_gpu(bias)
+        _same_device(logits, bias)
+        if bias.dtype != torch.float32 or bias.shape != (r.E,):
+            raise MoEFFNError(3, "bias must be float32 of shape [E]")
+    dev = logits.device
+    # sizes the library rejects are not allocated
+    shape = (r.T, K) if 0 < K <= 32 else (0, 0)
+    weights = torch.empty(shape, dtype=torch.float32, device=dev)
+    ids = torch.empty(shape, dtype=ids_dtype, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib.moe_ffn_router_fwd(ctypes.byref(r), _ptr(logits), _ptr(bias), _ptr(ids),
+                                      _ptr(weights), _stream(dev)))
+    return weights, ids
+
+
+def moe_ffn_router_bwd(d_topk_weights, logits, topk_ids, *, score: str = "softmax",
+                       renormalize: bool = True, scale: float = 1.0):
+    """d_logits [T, E] from d_topk_weights [T, K], the forward's logits and its
+    topk_ids.  ``score``, ``renormalize`` and ``scale`` are the forward's; bias
+    and groups only enter the selection, which has no gradient."""
+    lib = load_library()
+    _require_gpu(d_topk_weights, topk_ids)
+    _same_device(logits, d_topk_weights, topk_ids)
+    if topk_ids.dim() != 2 or logits.dim() != 2 or topk_ids.shape[0] != logits.shape[0]:
+        raise MoEFFNError(2, "expected logits [T, E] and topk_ids [T, K]")
+    if d_topk_weights.dtype != torch.float32 or d_topk_weights.shape != topk_ids.shape:
+        raise MoEFFNError(3, "d_topk_weights must be float32 with the shape of topk_ids")
+    r = _router(logits, topk_ids.shape[1], _ids_code(topk_ids), score, renormalize, 1, 1, 1, scale)
+    dev = logits.device
+    d_logits = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib.moe_ffn_router_bwd(ctypes.byref(r), _ptr(d_topk_weights), _ptr(logits),
+                                      _ptr(topk_ids), _ptr(d_logits), _stream(dev)))
+    return d_logits
+
+
+class MoERouterFunction(torch.autograd.Function):
+    """Autograd wrapper of the router: topk_weights is differentiable in logits;
+    topk_ids and the selection are not."""
+
+    @staticmethod
+    def forward(ctx, logits, K, bias, score, renormalize, groups, topk_groups, group_top, scale,
+                ids_dtype):
+        weights, ids = moe_ffn_router_fwd(logits, K, bias=bias, score=score,
+                                          renormalize=renormalize, groups=groups,
+                                          topk_groups=topk_groups, group_top=group_top,
+                                          scale=scale, ids_dtype=ids_dtype)
+        ctx.save_for_backward(logits, ids)
+        ctx.form = dict(score=score, renormalize=renormalize, scale=scale)
+        ctx.mark_non_differentiable(ids)
+        return weights, ids
+
+    @staticmethod
+    def backward(ctx, d_weights, _):
+        logits, ids = ctx.saved_tensors
+        d_logits = moe_ffn_router_bwd(d_weights.contiguous(), logits, ids, **ctx.form)
+        return (d_logits,) + (None,) * 9
+
+
+def moe_ffn_router(logits, K: int, *, bias=None, score: str = "softmax", renormalize: bool = True,
+                   groups: int = 1, topk_groups: int = 1, group_top: int = 1, scale: float = 1.0,
+                   ids_dtype=torch.int32):
+    """(topk_weights, topk_ids) for ``moe_ffn``; differentiable in logits."""
+    return MoERouterFunction.apply(logits, K, bias, score, renormalize, groups, topk_groups,
+                                   group_top, scale, ids_dtype)
+
+
+class MXFP4Weight:
+    """Expert weights [E, Kd, N] packed by ``moe_ffn_mxfp4_quantize``: ``data`` (uint8, the
+    library's layout), the sizes, the number of column panels and the dtype they came in."""
+
+    def __init__(self, data, E, Kd, N, panels, dtype):
+        self.data, self.E, self.Kd, self.N, self.panels, self.dtype = data, E, Kd, N, panels, dtype
+
+    def _stack(self):
+        return MXFP4Stack(self.E, self.Kd, self.N, self.panels,
+                          F32 if self.dtype == torch.float32 else BF16)
+
+
+def _mxfp4_weight_size(stack) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().moe_ffn_mxfp4_weight_size(ctypes.byref(stack), ctypes.byref(n)))
+    return n.value
+
+
+def moe_ffn_mxfp4_quantize(weight, panels: int = 1) -> MXFP4Weight:
+    """Pack expert weights [E, Kd, N] (float32 or bfloat16) as MXFP4 with blocks of 32 along Kd.
+
+    up_proj_weight [E, H, 2I] takes ``panels`` 2, down_proj_weight [E, I, H] 1."""
+    lib = load_library()
+    _require_gpu(weight)
+    if weight.dim() != 3:
+        raise MoEFFNError(2, "expected weight [E, Kd, N]")
+    E, Kd, N = weight.shape
+    stack = MXFP4Stack(E, Kd, N, panels, _dtype_code(weight))
+    dev = weight.device
+    data = torch.empty(_mxfp4_weight_size(stack), dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib.moe_ffn_mxfp4_quantize(ctypes.byref(stack), _ptr(weight), _ptr(data),
+                                          data.numel(), _stream(dev)))
+    return MXFP4Weight(data, E, Kd, N, panels, weight.dtype)
+
+
+def moe_ffn_mxfp4_dequantize(packed: MXFP4Weight):
+    """The values [E, Kd, N] that ``packed`` stands for, in the dtype it was packed from."""
+    lib = load_library()
+    _require_gpu(packed.data)
+    dev = packed.data.device
+    stack = packed._stack()
+    w = torch.empty((packed.E, packed.Kd, packed.N), dtype=packed.dtype, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib.moe_ffn_mxfp4_dequantize(ctypes.byref(stack), _ptr(packed.data),
+                                            packed.data.numel(), _ptr(w), _stream(dev)))
+    return w
+
+
+def _act_code(act: str) -> int:
+    if act not in ACT_FORMATS:
+        raise MoEFFNError(3, f"act must be one of {sorted(ACT_FORMATS)}, got {act!r}")
+    return ACT_FORMATS[act]
+
+
+def mxfp4_workspace_size(problem: Problem, act: str = "mxfp4", flags: int = 0) -> int:
+    ws = ctypes.c_size_t()
+    _check(load_library().moe_ffn_mxfp4_workspace_size(ctypes.byref(problem), _act_code(act),
+                                                       flags, ctypes.byref(ws)))
+    return ws.value
+
+
+def moe_ffn_mxfp4_fwd(x, topk_ids, topk_weights, up: MXFP4Weight, down: MXFP4Weight, *,
+                      act: str = "mxfp4", check_ids: bool = False, ws=None,
+                      return_ws: bool = False, flags: int = 0):
+    """y [T, H] of the layer on packed 4-bit weights (inference; include/moe_ffn.h,
+    moe_ffn_mxfp4_fwd).
+
+    ``act`` is the block format ("mxfp4" or "mxfp6") that the token rows and the SwiGLU output
+    are quantised to before their product.  ``ws`` may pass a preallocated workspace (uint8, at
+    least ``mxfp4_workspace_size`` bytes)."""
+    lib = load_library()
+    _require_gpu(x, topk_ids, topk_weights, up.data, down.data, ws)
+    _same_device(x, topk_ids, topk_weights, up.data, down.data, ws)
+    if x.dim() != 2 or topk_ids.dim() != 2 or topk_ids.shape[0] != x.shape[0]:
+        raise MoEFFNError(2, "expected x [T, H] and topk_ids [T, K]")
+    if topk_weights.dtype != torch.float32 or topk_weights.shape != topk_ids.shape:
+        raise MoEFFNError(3, "topk_weights must be float32 with the shape of topk_ids")
+    T, H = x.shape
+    E, I = down.E, down.Kd
+    if (up.E, up.Kd, up.N, up.panels) != (E, H, 2 * I, 2) or (down.N, down.panels) != (H, 1):
+        raise MoEFFNError(2, "expected up packed from [E, H, 2I] with 2 panels and down from "
+                             "[E, I, H] with 1")
+    prob = Problem(T, H, I, E, topk_ids.shape[1], _dtype_code(x), _ids_code(topk_ids))
+    flags |= CHECK_IDS if check_ids else 0
+    ws_bytes = mxfp4_workspace_size(prob, act, flags)
+    dev = x.device
+    y = torch.empty_like(x)
+    if ws is None:
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib.moe_ffn_mxfp4_fwd(ctypes.byref(prob), _act_code(act), _ptr(x), _ptr(topk_ids),
+                                     _ptr(topk_weights), _ptr(up.data), _ptr(down.data), _ptr(y),
+                                     _ptr(ws), ws.numel() * ws.element_size(), flags,
+                                     _stream(dev)))
+    return (y, ws) if return_ws else y
 
 
 def read_status(ws: torch.Tensor) -> int:

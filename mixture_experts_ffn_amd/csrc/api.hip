@@ -11,6 +11,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -18,6 +19,7 @@
 
 #include "kernels.h"
 #include "moe_ffn.h"
+#include "mx.h"
 
 static_assert(moe::MOE_DEV_BAD_ID == MOE_FFN_DEV_BAD_ID, "status bits");
 static_assert(moe::MOE_DEV_TIMEOUT == MOE_FFN_DEV_TIMEOUT, "status bits");
@@ -1200,6 +1202,380 @@ int moe_ffn_bwd_shared(const moe_ffn_problem *p, const void *dy, const void *x,
     return bwd_run(p, moe::BWD_STAGE_ALL, dy, x, topk_weights, up_proj_weight, down_proj_weight,
                    shared, saved, dx, d_up_proj_weight, d_down_proj_weight, d_topk_weights,
                    d_shared, ws, ws_bytes, flags, stream, ev);
+}
+
+// ---- router ------------------------------------------------------------------
+
+static int validate_router(const moe_ffn_router *r, moe::RouterArgs *a)
+{
+    if (!r)
+        return fail(MOE_FFN_ERR_NULL, "router is NULL");
+    if (r->logits_dtype != MOE_FFN_F32 && r->logits_dtype != MOE_FFN_BF16)
+        return fail(MOE_FFN_ERR_DTYPE, "logits_dtype must be F32 or BF16 (got %d)", r->logits_dtype);
+    if (r->ids_dtype != MOE_FFN_I32 && r->ids_dtype != MOE_FFN_I64)
+        return fail(MOE_FFN_ERR_DTYPE, "ids_dtype must be I32 or I64 (got %d)", r->ids_dtype);
+    if (r->E < 1 || r->E > 1024)
+        return fail(MOE_FFN_ERR_SHAPE, "E must be in [1, 1024] (got %lld)", (long long)r->E);
+    if (r->K < 1 || r->K > 32 || r->K > r->E)
+        return fail(MOE_FFN_ERR_SHAPE, "K must be in [1, min(32, E)] (got %lld)", (long long)r->K);
+    if (r->T < 0 || r->T >= (int64_t(1) << 31) || r->T * r->K >= (int64_t(1) << 31))
+        return fail(MOE_FFN_ERR_SHAPE, "T must be >= 0 with T*K < 2^31 (got %lld)", (long long)r->T);
+    if (r->logits_stride < r->E || r->logits_stride >= (int64_t(1) << 31))
+        return fail(MOE_FFN_ERR_SHAPE, "logits_stride must be in [E, 2^31) (got %lld)",
+                    (long long)r->logits_stride);
+    if (r->score != MOE_FFN_SCORE_SOFTMAX && r->score != MOE_FFN_SCORE_SIGMOID)
+        return fail(MOE_FFN_ERR_SHAPE, "score must be SOFTMAX or SIGMOID (got %d)", r->score);
+    if (r->renormalize != 0 && r->renormalize != 1)
+        return fail(MOE_FFN_ERR_SHAPE, "renormalize must be 0 or 1 (got %d)", r->renormalize);
+    if (r->groups < 1 || r->groups > 64 || r->E % r->groups)
+        return fail(MOE_FFN_ERR_SHAPE, "groups must be in [1, 64] and divide E (got %d)", r->groups);
+    if (r->topk_groups < 1 || r->topk_groups > r->groups)
+        return fail(MOE_FFN_ERR_SHAPE, "topk_groups must be in [1, groups] (got %d)",
+                    r->topk_groups);
+    if (r->K > r->topk_groups * (r->E / r->groups))
+        return fail(MOE_FFN_ERR_SHAPE, "K exceeds the experts of topk_groups groups");
+    if (r->group_top < 1 || r->group_top > 2 || (r->group_top == 2 && r->E / r->groups < 2))
+        return fail(MOE_FFN_ERR_SHAPE,
+                    "group_top must be 1, or 2 with two experts a group (got %d)", r->group_top);
+    if (!std::isfinite(r->scale))
+        return fail(MOE_FFN_ERR_SHAPE, "scale must be finite");
+    a->T = r->T;
+    a->stride = r->logits_stride;
+    a->E = (int)r->E;
+    a->K = (int)r->K;
+    a->groups = r->groups;
+    a->topk_groups = r->topk_groups;
+    a->group_top = r->group_top;
+    a->bf16 = r->logits_dtype == MOE_FFN_BF16;
+    a->ids64 = r->ids_dtype == MOE_FFN_I64;
+    a->sigmoid = r->score == MOE_FFN_SCORE_SIGMOID;
+    a->renorm = r->renormalize == 1;
+    a->scale = r->scale;
+    return MOE_FFN_OK;
+}
+
+int moe_ffn_router_fwd(const moe_ffn_router *r, const void *logits, const float *bias,
+                       void *topk_ids, float *topk_weights, void *stream)
+{
+    g_err[0] = 0;
+    moe::RouterArgs a{};
+    int rc = validate_router(r, &a);
+    if (rc)
+        return rc;
+    if (r->T == 0)
+        return MOE_FFN_OK;
+    if ((rc = check_ptr(logits, "logits", a.bf16 ? 2 : 4)) ||
+        (rc = check_ptr(topk_ids, "topk_ids", a.ids64 ? 8 : 4)) ||
+        (rc = check_ptr(topk_weights, "topk_weights", 4)) ||
+        (bias && (rc = check_ptr(bias, "bias", 4))))
+        return rc;
+    if ((rc = check_device()))
+        return rc;
+    a.logits = logits;
+    a.bias = bias;
+    a.ids = topk_ids;
+    a.weights = topk_weights;
+    HIP_TRY(moe::launch_router_fwd(a, static_cast<hipStream_t>(stream)), "router launch");
+    return MOE_FFN_OK;
+}
+
+int moe_ffn_router_bwd(const moe_ffn_router *r, const float *d_topk_weights, const void *logits,
+                       const void *topk_ids, void *d_logits, void *stream)
+{
+    g_err[0] = 0;
+    moe::RouterArgs a{};
+    int rc = validate_router(r, &a);
+    if (rc)
+        return rc;
+    if (r->T == 0)
+        return MOE_FFN_OK;
+    if ((rc = check_ptr(d_topk_weights, "d_topk_weights", 4)) ||
+        (rc = check_ptr(logits, "logits", a.bf16 ? 2 : 4)) ||
+        (rc = check_ptr(topk_ids, "topk_ids", a.ids64 ? 8 : 4)) ||
+        (rc = check_ptr(d_logits, "d_logits", a.bf16 ? 2 : 4)))
+        return rc;
+    if ((rc = check_device()))
+        return rc;
+    a.logits = logits;
+    a.ids = const_cast<void *>(topk_ids);
+    a.d_weights = d_topk_weights;
+    a.d_logits = d_logits;
+    HIP_TRY(moe::launch_router_bwd(a, static_cast<hipStream_t>(stream)), "router gradient launch");
+    return MOE_FFN_OK;
+}
+
+// ---- expert FFN on MXFP4 weights -----------------------------------------------
+
+namespace {
+
+struct MxWeightLayout {
+    size_t scales, total; // codes start at 0
+};
+
+MxWeightLayout mx_weight_layout(int64_t E, int64_t Kd, int64_t N, int panels)
+{
+    const moe::MxDims d(Kd, N / panels);
+    const size_t tiles = (size_t)E * panels * d.NT;
+    MxWeightLayout L;
+    L.scales = align_up(tiles * d.KS * 1024);
+    L.total = align_up(L.scales + tiles * d.KC * 256);
+    return L;
+}
+
+int validate_mx_weight(const moe_ffn_mxfp4_weight *w)
+{
+    if (!w)
+        return fail(MOE_FFN_ERR_NULL, "weight description is NULL");
+    if (w->dtype != MOE_FFN_F32 && w->dtype != MOE_FFN_BF16)
+        return fail(MOE_FFN_ERR_DTYPE, "dtype must be F32 or BF16 (got %d)", w->dtype);
+    if (w->E < 1 || w->E > 1024)
+        return fail(MOE_FFN_ERR_SHAPE, "E must be in [1, 1024] (got %lld)", (long long)w->E);
+    if (w->panels != 1 && w->panels != 2)
+        return fail(MOE_FFN_ERR_SHAPE, "panels must be 1 or 2 (got %d)", w->panels);
+    if (w->Kd < 8 || w->Kd % 8 || w->Kd >= (int64_t(1) << 31))
+        return fail(MOE_FFN_ERR_SHAPE, "Kd must be a positive multiple of 8 (got %lld)",
+                    (long long)w->Kd);
+    if (w->N < 8 || w->N % (8 * w->panels) || w->N >= (int64_t(1) << 31))
+        return fail(MOE_FFN_ERR_SHAPE, "N must be a positive multiple of 8 * panels (got %lld)",
+                    (long long)w->N);
+    if (w->Kd * w->N >= (int64_t(1) << 31))
+        return fail(MOE_FFN_ERR_SHAPE, "Kd*N must be < 2^31");
+    return MOE_FFN_OK;
+}
+
+struct MxFwdLayout {
+    moe::RoutePlan rp;
+    int BM;
+    int64_t max_mtiles;
+    moe::MxDims x, act;
+    size_t status, hist, bad, counts, offsets, mtile_off, mtile_expert, sorted_slot, slot_pos;
+    size_t x_codes, x_tails, x_scales, act_codes, act_tails, act_scales, o, total;
+};
+
+MxFwdLayout mx_fwd_layout(const moe_ffn_problem &p, int bits)
+{
+    MxFwdLayout L{{}, 32, 0, moe::MxDims(p.H, p.I), moe::MxDims(p.I, p.H)};
+    const int64_t TK = p.T * p.K;
+    const int E = (int)p.E;
+    L.rp = moe::make_route_plan(TK, E);
+    L.max_mtiles = moe::max_mtiles_bound(TK, E, L.BM);
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        size_t at = off;
+        off = align_up(off + (bytes ? bytes : 1));
+        return at;
+    };
+    L.status = take(sizeof(int32_t));
+    L.hist = take(sizeof(int32_t) * (size_t)E * (size_t)L.rp.NB);
+    L.bad = take(sizeof(int32_t) * (size_t)L.rp.NB);
+    L.counts = take(sizeof(int32_t) * (size_t)E);
+    L.offsets = take(sizeof(int32_t) * (size_t)(E + 1));
+    L.mtile_off = take(sizeof(int32_t) * (size_t)(E + 1));
+    L.mtile_expert = take(sizeof(int32_t) * (size_t)L.max_mtiles);
+    // padded like the bf16 forward's (routing fills whole blocks of it)
+    L.sorted_slot = take(sizeof(int32_t) * ((size_t)TK + 256));
+    L.slot_pos = take(sizeof(int32_t) * (size_t)TK);
+    L.x_codes = take((size_t)p.T * L.x.code_row());
+    L.x_tails = take((size_t)p.T * L.x.tail_row(bits));
+    L.x_scales = take((size_t)p.T * L.x.scale_row());
+    L.act_codes = take((size_t)TK * L.act.code_row());
+    L.act_tails = take((size_t)TK * L.act.tail_row(bits));
+    L.act_scales = take((size_t)TK * L.act.scale_row());
+    L.o = take(2 * (size_t)TK * (size_t)p.H);
+    L.total = off;
+    return L;
+}
+
+int validate_mx_fwd(const moe_ffn_problem *p, int32_t act_format, uint32_t flags)
+{
+    int rc = validate_problem(p);
+    if (rc)
+        return rc;
+    if (p->dtype != MOE_FFN_BF16)
+        return fail(MOE_FFN_ERR_DTYPE, "the MXFP4 forward supports BF16 only (got dtype %d)",
+                    p->dtype);
+    if (act_format != MOE_FFN_MXFP4 && act_format != MOE_FFN_MXFP6)
+        return fail(MOE_FFN_ERR_DTYPE, "act_format must be MXFP4 or MXFP6 (got %d)", act_format);
+    if (p->Is != 0)
+        return fail(MOE_FFN_ERR_SHAPE, "the MXFP4 forward takes no shared expert (Is must be 0)");
+    if (flags & ~(MOE_FFN_CHECK_IDS | MOE_FFN_CHECK_STATUS))
+        return fail(MOE_FFN_ERR_SHAPE, "flags: only CHECK_IDS and CHECK_STATUS apply (got 0x%x)",
+                    flags);
+    return MOE_FFN_OK;
+}
+
+} // namespace
+
+int moe_ffn_mxfp4_weight_size(const moe_ffn_mxfp4_weight *w, size_t *packed_bytes)
+{
+    g_err[0] = 0;
+    int rc = validate_mx_weight(w);
+    if (rc)
+        return rc;
+    if (!packed_bytes)
+        return fail(MOE_FFN_ERR_NULL, "packed_bytes is NULL");
+    *packed_bytes = mx_weight_layout(w->E, w->Kd, w->N, w->panels).total;
+    return MOE_FFN_OK;
+}
+
+static int mx_weight_run(const moe_ffn_mxfp4_weight *w, bool quantize, const void *weight,
+                         const void *packed, size_t packed_bytes, void *stream)
+{
+    g_err[0] = 0;
+    int rc = validate_mx_weight(w);
+    if (rc)
+        return rc;
+    const MxWeightLayout L = mx_weight_layout(w->E, w->Kd, w->N, w->panels);
+    if ((rc = check_ptr(weight, "weight")) || (rc = check_ptr(packed, "packed")))
+        return rc;
+    if (packed_bytes < L.total)
+        return fail(MOE_FFN_ERR_WORKSPACE, "packed buffer too small: %zu < %zu", packed_bytes,
+                    L.total);
+    if ((rc = check_device()))
+        return rc;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    char *codes = static_cast<char *>(const_cast<void *>(packed));
+    if (quantize)
+        HIP_TRY(moe::launch_mx_quantize_weight(w->dtype, weight, codes, codes + L.scales, w->E,
+                                               w->Kd, w->N, w->panels, s),
+                "quantisation launch");
+    else
+        HIP_TRY(moe::launch_mx_dequantize_weight(w->dtype, codes, codes + L.scales,
+                                                 const_cast<void *>(weight), w->E, w->Kd, w->N,
+                                                 w->panels, s),
+                "dequantisation launch");
+    return MOE_FFN_OK;
+}
+
+int moe_ffn_mxfp4_quantize(const moe_ffn_mxfp4_weight *w, const void *weight, void *packed,
+                           size_t packed_bytes, void *stream)
+{
+    return mx_weight_run(w, true, weight, packed, packed_bytes, stream);
+}
+
+int moe_ffn_mxfp4_dequantize(const moe_ffn_mxfp4_weight *w, const void *packed,
+                             size_t packed_bytes, void *weight, void *stream)
+{
+    return mx_weight_run(w, false, weight, packed, packed_bytes, stream);
+}
+
+int moe_ffn_mxfp4_workspace_size(const moe_ffn_problem *p, int32_t act_format, uint32_t flags,
+                                 size_t *ws_bytes)
+{
+    g_err[0] = 0;
+    int rc = validate_mx_fwd(p, act_format, flags);
+    if (rc)
+        return rc;
+    if (!ws_bytes)
+        return fail(MOE_FFN_ERR_NULL, "ws_bytes is NULL");
+    *ws_bytes = mx_fwd_layout(*p, act_format == MOE_FFN_MXFP4 ? 4 : 6).total;
+    return MOE_FFN_OK;
+}
+
+int moe_ffn_mxfp4_fwd(const moe_ffn_problem *p, int32_t act_format, const void *x,
+                      const void *topk_ids, const float *topk_weights, const void *up_packed,
+                      const void *down_packed, void *y, void *ws, size_t ws_bytes, uint32_t flags,
+                      void *stream)
+{
+    g_err[0] = 0;
+    int rc = validate_mx_fwd(p, act_format, flags);
+    if (rc)
+        return rc;
+    if (p->T == 0)
+        return MOE_FFN_OK;
+    const int bits = act_format == MOE_FFN_MXFP4 ? 4 : 6;
+    const MxFwdLayout L = mx_fwd_layout(*p, bits);
+    if ((rc = check_ptr(x, "x")) ||
+        (rc = check_ptr(topk_ids, "topk_ids", p->ids_dtype == MOE_FFN_I64 ? 8 : 4)) ||
+        (rc = check_ptr(topk_weights, "topk_weights", 4)) ||
+        (rc = check_ptr(up_packed, "up_packed")) || (rc = check_ptr(down_packed, "down_packed")) ||
+        (rc = check_ptr(y, "y")) || (rc = check_ptr(ws, "ws")))
+        return rc;
+    if (ws_bytes < L.total)
+        return fail(MOE_FFN_ERR_WORKSPACE, "workspace too small: %zu < %zu", ws_bytes, L.total);
+    int num_cus = 0;
+    if ((rc = check_device(&num_cus)))
+        return rc;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const int64_t TK = p->T * p->K;
+    const int E = (int)p->E;
+
+    HIP_TRY(moe::launch_mx_quantize_rows(bits, x, at<void>(ws, L.x_codes), at<void>(ws, L.x_tails),
+                                         at<void>(ws, L.x_scales), p->T, p->H, s),
+            "token quantisation launch");
+    moe::RouteBufs rb{};
+    rb.status = at<int32_t>(ws, L.status);
+    rb.hist = at<int32_t>(ws, L.hist);
+    rb.bad = at<int32_t>(ws, L.bad);
+    rb.counts = at<int32_t>(ws, L.counts);
+    rb.offsets = at<int32_t>(ws, L.offsets);
+    rb.mtile_off = at<int32_t>(ws, L.mtile_off);
+    rb.mtile_expert = at<int32_t>(ws, L.mtile_expert);
+    rb.sorted_slot = at<int32_t>(ws, L.sorted_slot);
+    rb.slot_pos = at<int32_t>(ws, L.slot_pos);
+    rb.T = p->T;
+    HIP_TRY(moe::launch_route(topk_ids, p->ids_dtype == MOE_FFN_I64, TK, E, L.BM, L.rp, rb, s),
+            "route launch");
+    if (flags & MOE_FFN_CHECK_IDS) {
+        int32_t st = 0;
+        HIP_TRY(hipMemcpyAsync(&st, rb.status, sizeof st, hipMemcpyDeviceToHost, s), "status copy");
+        HIP_TRY(hipStreamSynchronize(s), "stream sync");
+        if (st)
+            return fail(MOE_FFN_ERR_EXPERT_ID, "topk_ids holds a value outside [0, %d)", E);
+    }
+
+    moe::MxGemmArgs g{};
+    g.sorted_slot = rb.sorted_slot;
+    g.offsets = rb.offsets;
+    g.mtile_off = rb.mtile_off;
+    g.mtile_expert = rb.mtile_expert;
+    g.max_mtiles = (int)L.max_mtiles;
+    g.E = E;
+    g.topk = (int)p->K;
+    g.act_codes = at<uint8_t>(ws, L.act_codes);
+    g.act_tails = at<uint8_t>(ws, L.act_tails);
+    g.act_scales = at<uint8_t>(ws, L.act_scales);
+    g.act_KS = L.act.KS;
+    g.act_KC = L.act.KC;
+    g.o = at<void>(ws, L.o);
+
+    moe::MxGemmArgs g1 = g;
+    const MxWeightLayout up = mx_weight_layout(p->E, p->H, 2 * p->I, 2);
+    g1.wcodes = static_cast<const uint8_t *>(up_packed);
+    g1.wscales = g1.wcodes + up.scales;
+    g1.acodes = at<uint8_t>(ws, L.x_codes);
+    g1.atails = at<uint8_t>(ws, L.x_tails);
+    g1.ascales = at<uint8_t>(ws, L.x_scales);
+    g1.N = (int)p->I;
+    g1.NT = L.x.NT;
+    g1.KS = L.x.KS;
+    g1.KC = L.x.KC;
+    HIP_TRY(moe::launch_mx_gemm(true, bits, g1, num_cus, s), "gemm1 launch");
+
+    moe::MxGemmArgs g2 = g;
+    const MxWeightLayout down = mx_weight_layout(p->E, p->I, p->H, 1);
+    g2.wcodes = static_cast<const uint8_t *>(down_packed);
+    g2.wscales = g2.wcodes + down.scales;
+    g2.acodes = g.act_codes;
+    g2.atails = g.act_tails;
+    g2.ascales = g.act_scales;
+    g2.N = (int)p->H;
+    g2.NT = L.act.NT;
+    g2.KS = L.act.KS;
+    g2.KC = L.act.KC;
+    HIP_TRY(moe::launch_mx_gemm(false, bits, g2, num_cus, s), "gemm2 launch");
+
+    HIP_TRY(moe::launch_combine(MOE_FFN_BF16, g.o, rb.slot_pos, topk_weights, y, p->T, (int)p->H,
+                                (int)p->K, rb.offsets, E, 0, s),
+            "combine launch");
+    if (flags & MOE_FFN_CHECK_STATUS) {
+        int32_t st = 0;
+        HIP_TRY(hipMemcpyAsync(&st, rb.status, sizeof st, hipMemcpyDeviceToHost, s), "status copy");
+        HIP_TRY(hipStreamSynchronize(s), "stream sync");
+        if (st & moe::MOE_DEV_BAD_ID)
+            return fail(MOE_FFN_ERR_EXPERT_ID, "topk_ids holds a value outside [0, %d)", E);
+    }
+    return MOE_FFN_OK;
 }
 
 int moe_ffn_read_status(const void *ws, void *stream, int32_t *device_status)

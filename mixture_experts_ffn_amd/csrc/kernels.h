@@ -202,6 +202,46 @@ int engine_dgp_width(int I); // columns of the B2 partial-dot buffer
 void engine_feature_tiling(int kind, int M, int N, int num_cus, int *tiles_per_expert,
                            int *wg_per_xcd);
 
+// ---- MXFP4 expert FFN (layouts: mx.h) ---------------------------------------------
+hipError_t launch_mx_quantize_weight(int dtype, const void *w, void *codes, void *scales, int64_t E,
+                                     int64_t Kd, int64_t N, int panels, hipStream_t s);
+hipError_t launch_mx_dequantize_weight(int dtype, const void *codes, const void *scales, void *w,
+                                       int64_t E, int64_t Kd, int64_t N, int panels, hipStream_t s);
+// x [T, H] bf16 -> codes of `bits` (4 or 6) bits and scales, row-major
+hipError_t launch_mx_quantize_rows(int bits, const void *x, void *codes, void *tails, void *scales,
+                                   int64_t T, int64_t H, hipStream_t s);
+struct MxGemmArgs {
+    const uint8_t *wcodes, *wscales; // packed weights (GEMM1: two panels)
+    const uint8_t *acodes, *atails, *ascales; // GEMM1: token rows; GEMM2: act rows (permuted)
+    uint8_t *act_codes, *act_tails, *act_scales; // GEMM1's output, permuted rows
+    void *o;                         // GEMM2's output [TK, N] bf16
+    const int32_t *sorted_slot;      // permuted row -> slot
+    const int32_t *offsets;          // [E + 1]
+    const int32_t *mtile_off;        // [E + 1]
+    const int32_t *mtile_expert;     // [max_mtiles]
+    int E, topk, N;                  // N: output columns (I or H)
+    int NT, KS, KC;                  // column tiles of a panel; k-steps and chunks
+    int act_KS, act_KC;              // of GEMM1's output rows
+    int max_mtiles;
+};
+hipError_t launch_mx_gemm(bool g1, int bits, const MxGemmArgs &a, int num_cus, hipStream_t s);
+
+// ---- router -----------------------------------------------------------------------
+struct RouterArgs {
+    const void *logits;   // [T, E], rows `stride` apart
+    const float *bias;    // [E] or null
+    void *ids;            // [T, K] int32 or int64
+    float *weights;       // forward: gates [T, K]
+    const float *d_weights; // backward
+    void *d_logits;       // backward: [T, E], rows E apart
+    int64_t T, stride;
+    int E, K, groups, topk_groups, group_top;
+    bool bf16, ids64, sigmoid, renorm;
+    float scale;
+};
+hipError_t launch_router_fwd(const RouterArgs &a, hipStream_t s);
+hipError_t launch_router_bwd(const RouterArgs &a, hipStream_t s);
+
 // ---- combine ---------------------------------------------------------------------
 // y[t] = Σ_k g[t, k] o[slot_pos[tK+k]] + Σ_c o[offsets[Er] + cT + t] (the S
 // shared-expert chunks, gate 1, after the routed terms; S = 0: none)

@@ -1,0 +1,186 @@
+// mx.hip — MXFP4 quantisation of expert weights and its inverse, and the
+// per-call quantisation of the token rows (formats and layouts: mx.h).
+//
+// All three are single passes bound by HBM: a weight of n values moves 2n (or
+// 4n) + 17n/32 bytes in either direction, a token row 2H + 17H/32 (MXFP4) or
+// 2H + 25H/32 (MXFP6).
+#include "kernels.h"
+#include "mx.h"
+
+namespace moe {
+
+// Weights.  A block of 32 runs down a column, so a thread owns one (column,
+// k-block): its 32 loads are coalesced across the columns of the wave, the
+// maximum needs no other lane, and its 32 codes are the 16 bytes of one lane
+// of one k-step in the packed layout.  Lanes follow that layout (32 columns of
+// k-block 2s, then the same columns of 2s + 1), so a wave writes 1024
+// contiguous bytes.  Grid: (column tile, group of 8 k-steps, expert * panel),
+// two k-steps per wave.
+template <typename T>
+__global__ __launch_bounds__(256) void mx_quantize_weight_kernel(
+    const T *__restrict__ w, u32x4 *__restrict__ codes, uint8_t *__restrict__ scales, int Kd, int N,
+    int panels, int NT, int KS, int KC)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int tile = blockIdx.x;
+    const int64_t ep = blockIdx.z;
+    const int e = (int)(ep / panels), panel = (int)(ep % panels);
+    const int pc = N / panels;
+    const int col = tile * 32 + (lane & 31);
+    const T *base = w + (int64_t)e * Kd * N + (int64_t)panel * pc + col;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const int ks = blockIdx.y * 8 + s * 4 + wave;
+        if (ks >= KS)
+            return;
+        const int k0 = ks * 64 + (lane >> 5) * 32;
+        float v[32];
+        uint32_t top = 0;
+        if (col < pc && k0 + 32 <= Kd) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                v[i] = to_f32<T>(base[(int64_t)(k0 + i) * N]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                v[i] = col < pc && k0 + i < Kd ? to_f32<T>(base[(int64_t)(k0 + i) * N]) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            top = max(top, abs_bits(v[i]));
+        const int code = mx_scale_code(top);
+        const float inv = mx_inverse(code);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            v[i] *= inv;
+        u32x4 out;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            out[i] = mx_pack8_fp4(v + 8 * i);
+        const int64_t t = ep * NT + tile;
+        codes[(t * KS + ks) * 64 + lane] = out;
+        scales[((t * KC + (ks >> 2)) * 64 + lane) * 4 + (ks & 3)] = (uint8_t)code;
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void mx_dequantize_weight_kernel(
+    const u32x4 *__restrict__ codes, const uint8_t *__restrict__ scales, T *__restrict__ w, int Kd,
+    int N, int panels, int NT, int KS, int KC)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int tile = blockIdx.x;
+    const int64_t ep = blockIdx.z;
+    const int e = (int)(ep / panels), panel = (int)(ep % panels);
+    const int pc = N / panels;
+    const int col = tile * 32 + (lane & 31);
+    T *base = w + (int64_t)e * Kd * N + (int64_t)panel * pc + col;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const int ks = blockIdx.y * 8 + s * 4 + wave;
+        if (ks >= KS)
+            return;
+        const int k0 = ks * 64 + (lane >> 5) * 32;
+        const int64_t t = ep * NT + tile;
+        const u32x4 c = codes[(t * KS + ks) * 64 + lane];
+        const float x = mx_scale_value(scales[((t * KC + (ks >> 2)) * 64 + lane) * 4 + (ks & 3)]);
+        if (col >= pc)
+            continue;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (k0 + i < Kd)
+                base[(int64_t)(k0 + i) * N] = from_f32<T>(mx_fp4_value(c[i / 8] >> (4 * (i % 8)) & 15) * x);
+    }
+}
+
+// Token rows x [T, H] bf16 -> row-major codes and scales.  A lane owns a block:
+// its maximum needs no other lane and its codes are whole vectors.  The row is
+// padded with zeros to whole k-steps.
+template <int BITS>
+__global__ __launch_bounds__(256) void mx_quantize_rows_kernel(
+    const bf16 *__restrict__ x, u32x4 *__restrict__ codes, u32x2 *__restrict__ tails,
+    uint8_t *__restrict__ scales, int64_t T, int H, int KS, int KC)
+{
+    const int64_t n = T * (2 * KS);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n;
+         i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / (2 * KS);
+        const int b = (int)(i - t * (2 * KS));
+        float v[32];
+        uint32_t top = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            u32x4 raw = {0u, 0u, 0u, 0u};
+            if (b * 32 + q * 8 < H) // H is a multiple of 8
+                raw = *reinterpret_cast<const u32x4 *>(x + t * H + b * 32 + q * 8);
+            const bf16 *vv = reinterpret_cast<const bf16 *>(&raw);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[q * 8 + j] = static_cast<float>(vv[j]);
+                top = max(top, abs_bits(v[q * 8 + j]));
+            }
+        }
+        const int code = mx_scale_code(top);
+        const float inv = mx_inverse(code);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            v[j] *= inv;
+        if constexpr (BITS == 4) {
+            codes[i] = u32x4{mx_pack8_fp4(v), mx_pack8_fp4(v + 8), mx_pack8_fp4(v + 16),
+                             mx_pack8_fp4(v + 24)};
+        } else {
+            const u32x6 c = mx_pack_fp6<32>(v);
+            codes[i] = u32x4{c[0], c[1], c[2], c[3]};
+            tails[i] = u32x2{c[4], c[5]};
+        }
+        scales[t * (KC * 8) + mx_scale_at(b)] = (uint8_t)code;
+    }
+}
+
+template <typename T>
+static hipError_t weight_t(bool quantize, const void *src, void *codes, void *scales, void *dst,
+                           int64_t E, int64_t Kd, int64_t N, int panels, hipStream_t s)
+{
+    const MxDims d(Kd, N / panels);
+    // grid.z carries at most 65535 (expert, panel) pairs; E <= 1024, panels <= 2
+    const dim3 grid((unsigned)d.NT, (unsigned)((d.KS + 7) / 8), (unsigned)(E * panels));
+    if (quantize)
+        hipLaunchKernelGGL(mx_quantize_weight_kernel<T>, grid, dim3(256), 0, s,
+                           static_cast<const T *>(src), static_cast<u32x4 *>(codes),
+                           static_cast<uint8_t *>(scales), (int)Kd, (int)N, panels, d.NT, d.KS, d.KC);
+    else
+        hipLaunchKernelGGL(mx_dequantize_weight_kernel<T>, grid, dim3(256), 0, s,
+                           static_cast<const u32x4 *>(codes), static_cast<const uint8_t *>(scales),
+                           static_cast<T *>(dst), (int)Kd, (int)N, panels, d.NT, d.KS, d.KC);
+    return hipGetLastError();
+}
+
+hipError_t launch_mx_quantize_weight(int dtype, const void *w, void *codes, void *scales, int64_t E,
+                                     int64_t Kd, int64_t N, int panels, hipStream_t s)
+{
+    return dtype == 1 ? weight_t<bf16>(true, w, codes, scales, nullptr, E, Kd, N, panels, s)
+                      : weight_t<float>(true, w, codes, scales, nullptr, E, Kd, N, panels, s);
+}
+
+hipError_t launch_mx_dequantize_weight(int dtype, const void *codes, const void *scales, void *w,
+                                       int64_t E, int64_t Kd, int64_t N, int panels, hipStream_t s)
+{
+    void *c = const_cast<void *>(codes), *x = const_cast<void *>(scales);
+    return dtype == 1 ? weight_t<bf16>(false, nullptr, c, x, w, E, Kd, N, panels, s)
+                      : weight_t<float>(false, nullptr, c, x, w, E, Kd, N, panels, s);
+}
+
+hipError_t launch_mx_quantize_rows(int bits, const void *x, void *codes, void *tails, void *scales,
+                                   int64_t T, int64_t H, hipStream_t s)
+{
+    const MxDims d(H, 32);
+    const int64_t blocks = (T * d.KS * 2 + 255) / 256;
+    const dim3 grid((unsigned)(blocks < 8192 ? blocks : 8192));
+    auto k = bits == 4 ? mx_quantize_rows_kernel<4> : mx_quantize_rows_kernel<6>;
+    hipLaunchKernelGGL(k, grid, dim3(256), 0, s, static_cast<const bf16 *>(x),
+                       static_cast<u32x4 *>(codes), static_cast<u32x2 *>(tails),
+                       static_cast<uint8_t *>(scales), T, (int)H, d.KS, d.KC);
+    return hipGetLastError();
+}
+
+} // namespace moe
