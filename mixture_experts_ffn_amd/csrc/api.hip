@@ -1352,9 +1352,16 @@ struct MxFwdLayout {
     size_t x_codes, x_tails, x_scales, act_codes, act_tails, act_scales, o, total;
 };
 
+// Rows of an M-tile from the mean rows per expert.
+int mx_tile_rows(const moe_ffn_problem &p)
+{
+    const double rows = (double)(p.T * p.K) / (double)p.E;
+    return rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 1024 ? 128 : 256;
+}
+
 MxFwdLayout mx_fwd_layout(const moe_ffn_problem &p, int bits)
 {
-    MxFwdLayout L{{}, 32, 0, moe::MxDims(p.H, p.I), moe::MxDims(p.I, p.H)};
+    MxFwdLayout L{{}, mx_tile_rows(p), 0, moe::MxDims(p.H, p.I), moe::MxDims(p.I, p.H)};
     const int64_t TK = p.T * p.K;
     const int E = (int)p.E;
     L.rp = moe::make_route_plan(TK, E);
@@ -1536,7 +1543,8 @@ int moe_ffn_mxfp4_fwd(const moe_ffn_problem *p, int32_t act_format, const void *
     g.act_tails = at<uint8_t>(ws, L.act_tails);
     g.act_scales = at<uint8_t>(ws, L.act_scales);
     g.act_KS = L.act.KS;
-    g.act_KC = L.act.KC;
+    g.act_srow = L.act.scale_row();
+    g.BM = L.BM;
     g.o = at<void>(ws, L.o);
 
     moe::MxGemmArgs g1 = g;
@@ -1550,6 +1558,7 @@ int moe_ffn_mxfp4_fwd(const moe_ffn_problem *p, int32_t act_format, const void *
     g1.NT = L.x.NT;
     g1.KS = L.x.KS;
     g1.KC = L.x.KC;
+    g1.srow = L.x.scale_row();
     HIP_TRY(moe::launch_mx_gemm(true, bits, g1, num_cus, s), "gemm1 launch");
 
     moe::MxGemmArgs g2 = g;
@@ -1563,6 +1572,7 @@ int moe_ffn_mxfp4_fwd(const moe_ffn_problem *p, int32_t act_format, const void *
     g2.NT = L.act.NT;
     g2.KS = L.act.KS;
     g2.KC = L.act.KC;
+    g2.srow = L.act.scale_row();
     HIP_TRY(moe::launch_mx_gemm(false, bits, g2, num_cus, s), "gemm2 launch");
 
     HIP_TRY(moe::launch_combine(MOE_FFN_BF16, g.o, rb.slot_pos, topk_weights, y, p->T, (int)p->H,

@@ -8,6 +8,7 @@
 // of 32 act columns is two lanes' registers and its scale needs one exchange.
 #include "kernels.h"
 #include "mx.h"
+#include "tile_common.h"
 
 namespace moe {
 
@@ -66,7 +67,7 @@ template <int BITS> __device__ inline ActRow act_row(const MxGemmArgs &a, int64_
 {
     return {a.act_codes + row * (a.act_KS * 32),
             BITS == 6 ? a.act_tails + row * (a.act_KS * 16) : nullptr,
-            a.act_scales + row * (a.act_KC * 8)};
+            a.act_scales + row * a.act_srow};
 }
 
 // SwiGLU of one 32-column block of one token and its quantisation.  The 32
@@ -111,16 +112,17 @@ __device__ inline void store_act(const f32x16 &g, const f32x16 &u, const ActRow 
         r.scales[mx_scale_at(block)] = (uint8_t)code;
 }
 
-// The block behind the last one where their number is odd (the second half of
-// the last k-step).
-template <int BITS> __device__ inline void store_empty(const ActRow &r, int block)
+// The up to three blocks from `block` to the end of the row's last k-step pair.
+template <int BITS> __device__ inline void store_empty(const ActRow &r, int block, int end)
 {
     const int h = (threadIdx.x >> 5) & 1;
-    *reinterpret_cast<u32x2 *>(r.codes + block * 16 + h * 8) = u32x2{0u, 0u};
-    if (h == 0) {
-        if constexpr (BITS == 6)
-            *reinterpret_cast<u32x2 *>(r.tails + block * 8) = u32x2{0u, 0u};
-        r.scales[mx_scale_at(block)] = 0;
+    for (; block < end; ++block) {
+        *reinterpret_cast<u32x2 *>(r.codes + block * 16 + h * 8) = u32x2{0u, 0u};
+        if (h == 0) {
+            if constexpr (BITS == 6)
+                *reinterpret_cast<u32x2 *>(r.tails + block * 8) = u32x2{0u, 0u};
+            r.scales[mx_scale_at(block)] = 0;
+        }
     }
 }
 
@@ -151,7 +153,7 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxGemmArgs a)
         const int64_t arow = G1 ? a.sorted_slot[row] / a.topk : row;
         const uint8_t *ac = a.acodes + arow * (a.KS * 32) + h * 16;
         const uint8_t *at = BITS == 6 ? a.atails + arow * (a.KS * 16) + h * 8 : nullptr;
-        const uint8_t *as = a.ascales + arow * (a.KC * 8) + h * 4;
+        const uint8_t *as = a.ascales + arow * a.srow + h * 4;
         const uint8_t *wc[4], *ws[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -240,8 +242,8 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxGemmArgs a)
                 const int c = cg * 2 + (wave >> 1);
                 const ActRow r = act_row<BITS>(a, row);
                 store_act<BITS>(sum, up, r, c, live && c < a.NT);
-                if (c == a.NT - 1 && c + 1 < 2 * a.act_KS && live)
-                    store_empty<BITS>(r, c + 1);
+                if (c == a.NT - 1 && live)
+                    store_empty<BITS>(r, c + 1, 2 * a.act_KS);
             }
         } else {
             const int c = cg * 4 + wave;
@@ -261,16 +263,238 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxGemmArgs a)
     }
 }
 
+// Tile kernel.  A tile is 32 TF token rows of one expert times eight column
+// tiles, two a wave: GEMM1 a gate tile and the up tile of the same columns (so
+// the epilogue stays in the wave), GEMM2 two neighbours.  The weights go from
+// memory straight into registers, since the waves share none; the token rows,
+// which all four waves read, are copied into a ring of LDS stages of two
+// k-steps, 64 bytes of codes a row, swizzled like the bf16 kernels' rows.
+template <int BITS, bool G1, int TF>
+__global__ __launch_bounds__(256, TF == 8 ? 1 : 2) void mx_tile_kernel(MxGemmArgs a)
+{
+    using namespace tile;
+    constexpr int ROWS = TF * 32;
+    constexpr int CODES = ROWS * 64, TAILS = BITS == 6 ? ROWS * 32 : 0, SCALES = ROWS * 16;
+    constexpr int STAGE = CODES + TAILS, RING = 4;
+    constexpr int NC = TF / 2;                       // code copies of a wave and stage
+    constexpr int NTL = BITS == 6 ? (TF + 3) / 4 : 0; // tail copies
+    constexpr int NL = 4;                            // weight loads of a wave and stage
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[RING * STAGE + 2 * SCALES];
+    unsigned char *const sscale = smem + RING * STAGE;
+    const int lane = threadIdx.x & 63;
+    const int wave = uni(threadIdx.x >> 6);
+    const int h = lane >> 5, fr = lane & 31;
+    constexpr int PER = G1 ? 4 : 8; // column tiles of a panel
+    const int ncg = (a.NT + PER - 1) / PER;
+    const int KP = a.KS >> 1; // stages
+    const int64_t total = (int64_t)uni(ldc(a.mtile_off, a.E)) * ncg;
+    const int xcd = blockIdx.x & 7;
+    const int64_t t1 = total * (xcd + 1) / 8;
+    for (int64_t t = total * xcd / 8 + (blockIdx.x >> 3); t < t1; t += gridDim.x >> 3) {
+        // expert-major; inside an expert groups of up to 8 M-tiles, column
+        // groups outer and M-tiles inner, so that tiles in flight share weights
+        const int e = ldc(a.mtile_expert, (int)(t / ncg));
+        const int mt0 = ldc(a.mtile_off, e), mts = ldc(a.mtile_off, e + 1) - mt0;
+        const int64_t local = t - (int64_t)mt0 * ncg;
+        const int grp = (int)(local / (8 * ncg));
+        const int gm = min(mts - grp * 8, 8);
+        const int rr = (int)(local - (int64_t)grp * 8 * ncg);
+        const int cg = uni(rr / gm);
+        const int mt = grp * 8 + rr % gm;
+        const int r0 = ldc(a.offsets, e) + mt * ROWS;
+        const int nr = min(ROWS, ldc(a.offsets, e + 1) - r0);
+
+        auto row_of = [&](int r) -> int64_t {
+            const int p = r0 + min(r, nr - 1);
+            return G1 ? a.sorted_slot[p] / a.topk : p;
+        };
+        // a copy moves 1024 bytes: 16 rows of codes, 32 of tails, 64 of scales
+        const uint8_t *src_c[NC], *src_t[NTL + 1], *src_s;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int r = (wave * NC + i) * 16 + (lane >> 2);
+            src_c[i] = a.acodes + row_of(r) * (a.KS * 32) + aswz<4>(r, lane & 3) * 16;
+        }
+#pragma unroll
+        for (int i = 0; i < NTL; ++i) {
+            const int r = ((wave * NTL + i) * 32 + (lane >> 1)) & (ROWS - 1);
+            src_t[i] = a.atails + row_of(r) * (a.KS * 16) + (lane & 1) * 16;
+        }
+        src_s = a.ascales + row_of((wave * 64 + lane) & (ROWS - 1)) * a.srow;
+        const uint8_t *wc[2], *ws[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int c = min(cg * PER + (G1 ? wave : 2 * wave + j), a.NT - 1);
+            const int64_t tile = ((int64_t)e * (G1 ? 2 : 1) + (G1 ? j : 0)) * a.NT + c;
+            wc[j] = a.wcodes + tile * a.KS * 1024;
+            ws[j] = a.wscales + tile * a.KC * 256;
+        }
+        const uint32_t wl = lane * 16, sl = lane * 4;
+        // copies of stage p (past the end: of the last one, into a stage that is not read again)
+        auto copy = [&](int p) {
+            unsigned char *st = smem + (p & (RING - 1)) * STAGE;
+            const int q = min(p, KP - 1);
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                g2l16(src_c[i] + q * 64, (lds_void *)(st + (wave * NC + i) * 1024));
+#pragma unroll
+            for (int i = 0; i < NTL; ++i)
+                if (TF >= 4 || wave < 2)
+                    g2l16(src_t[i] + q * 32, (lds_void *)(st + CODES + (wave * NTL + i) * 1024));
+        };
+        // scales of the four stages 4g .. 4g + 3
+        auto copy_scales = [&](int g) {
+            if (wave < TF / 2)
+                g2l16(src_s + g * 16, (lds_void *)(sscale + (g & 1) * SCALES + wave * 1024));
+        };
+        struct W {
+            u32x4 c[2][2];
+        };
+        auto load_w = [&](int p, W &w) {
+            const int64_t at = (int64_t)min(p, KP - 1) * 2048;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    w.c[j][s] = *reinterpret_cast<const u32x4 *>(wc[j] + at + s * 1024 + wl);
+        };
+        struct S {
+            int w[2];
+        };
+        auto load_s = [&](int kc, S &s) {
+            const int64_t at = (int64_t)min(kc, a.KC - 1) * 256;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                s.w[j] = *reinterpret_cast<const int *>(ws[j] + at + sl);
+        };
+        f32x16 acc[2][TF];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int f = 0; f < TF; ++f)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    acc[j][f][i] = 0.f;
+        // the two k-steps of stage p; ODD: the second half of the scale dwords
+        auto compute = [&](int p, const W &w, const S &sw, auto ODD) {
+            const unsigned char *st = smem + (p & (RING - 1)) * STAGE;
+            const unsigned char *sc = sscale + ((p >> 2) & 1) * SCALES + ((p >> 1) & 1) * 8 + h * 4;
+            int as[TF];
+#pragma unroll
+            for (int f = 0; f < TF; ++f)
+                as[f] = *reinterpret_cast<const int *>(sc + (f * 32 + fr) * 16);
+            auto step = [&](auto H) {
+                constexpr int s = decltype(H)::value;
+                constexpr int sel = 2 * decltype(ODD)::value + s;
+#pragma unroll
+                for (int f = 0; f < TF; ++f) {
+                    const int r = f * 32 + fr;
+                    MxFrag<BITS> av;
+                    av.c = *reinterpret_cast<const u32x4 *>(st + r * 64 + aswz<4>(r, 2 * s + h) * 16);
+                    if constexpr (BITS == 6)
+                        av.t = *reinterpret_cast<const u32x2 *>(st + CODES + r * 32 + s * 16 + h * 8);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[j][f] = mx_mma<BITS, sel>(w.c[j][s], sw.w[j], av, as[f], acc[j][f]);
+                }
+            };
+            step(IC<0>{});
+            step(IC<1>{});
+        };
+        W w0, w1;
+        S s0, s1;
+        copy_scales(0);
+        copy(0);
+        load_w(0, w0);
+        load_s(0, s0);
+        copy(1);
+        load_w(1, w1);
+        wait_vm<NC + NTL + NL>();
+        lds_barrier();
+        // Stage p: its copies and weights were issued two stages ago.  The
+        // copies of p + 2 precede the weights' loads of p + 2, so waiting for
+        // all but the youngest operations covers the copies of p + 1.
+        constexpr int YOUNG = 2 * NL + NC + (TF >= 4 ? NTL : 0);
+        int p = 0;
+        for (; p + 2 <= KP; p += 2) {
+            if ((p & 3) == 0)
+                copy_scales((p >> 2) + 1);
+            copy(p + 2);
+            compute(p, w0, s0, IC<0>{});
+            load_w(p + 2, w0);
+            load_s((p >> 1) + 1, s1);
+            wait_vm<YOUNG>();
+            lds_barrier();
+            copy(p + 3);
+            compute(p + 1, w1, s0, IC<1>{});
+            load_w(p + 3, w1);
+            s0 = s1;
+            wait_vm<YOUNG>();
+            lds_barrier();
+        }
+        if (p < KP)
+            compute(p, w0, s0, IC<0>{});
+        wait_vm<0>();
+        lds_barrier();
+        // the last barrier: every wave is past its reads, so the next tile may copy
+        if constexpr (G1) {
+            const int c = cg * 4 + wave;
+#pragma unroll
+            for (int f = 0; f < TF; ++f) {
+                const int r = f * 32 + fr;
+                const bool live = r < nr && c < a.NT;
+                const ActRow ar = act_row<BITS>(a, r0 + min(r, nr - 1));
+                store_act<BITS>(acc[0][f], acc[1][f], ar, c, live);
+                if (c == a.NT - 1 && live)
+                    store_empty<BITS>(ar, c + 1, 2 * a.act_KS);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int col = (cg * 8 + 2 * wave + j) * 32 + 16 * h;
+#pragma unroll
+                for (int f = 0; f < TF; ++f) {
+                    const int r = f * 32 + fr;
+                    float v[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        v[i] = acc[j][f][i];
+                    gather_columns(v);
+                    bf16x8 o[2];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        o[i / 8][i % 8] = (bf16)v[i];
+                    bf16 *dst = static_cast<bf16 *>(a.o) + (int64_t)(r0 + r) * a.N + col;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) // N is a multiple of 8
+                        if (r < nr && col + 8 * i < a.N)
+                            *reinterpret_cast<bf16x8 *>(dst + 8 * i) = o[i];
+                }
+            }
+        }
+    }
+}
+
+template <int BITS, bool G1> static auto tile_kernel(int BM)
+{
+    return BM == 64 ? mx_tile_kernel<BITS, G1, 2>
+           : BM == 128 ? mx_tile_kernel<BITS, G1, 4>
+                       : mx_tile_kernel<BITS, G1, 8>;
+}
+
 hipError_t launch_mx_gemm(bool g1, int bits, const MxGemmArgs &a, int num_cus, hipStream_t s)
 {
-    const int per = g1 ? 2 : 4;
+    const bool stream = a.BM == 32;
+    const int per = stream ? (g1 ? 2 : 4) : (g1 ? 4 : 8);
     const int64_t most = (int64_t)a.max_mtiles * ((a.NT + per - 1) / per);
-    int64_t grid = (int64_t)num_cus * 16;
+    int64_t grid = (int64_t)num_cus * (stream ? 16 : a.BM == 256 ? 1 : 2);
     if (most < grid)
         grid = most;
-    grid = (grid + 7) / 8 * 8;
-    auto k = g1 ? (bits == 4 ? mx_stream_kernel<4, true> : mx_stream_kernel<6, true>)
-                : (bits == 4 ? mx_stream_kernel<4, false> : mx_stream_kernel<6, false>);
+    grid = (grid + 7) / 8 * 8; // a whole number of workgroups for each XCD
+    auto k = stream ? (g1 ? (bits == 4 ? mx_stream_kernel<4, true> : mx_stream_kernel<6, true>)
+                          : (bits == 4 ? mx_stream_kernel<4, false> : mx_stream_kernel<6, false>))
+             : g1   ? (bits == 4 ? tile_kernel<4, true>(a.BM) : tile_kernel<6, true>(a.BM))
+                    : (bits == 4 ? tile_kernel<4, false>(a.BM) : tile_kernel<6, false>(a.BM));
     hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(256), 0, s, a);
     return hipGetLastError();
 }

@@ -221,8 +221,10 @@ struct MxGemmArgs {
     const int32_t *mtile_expert;     // [max_mtiles]
     int E, topk, N;                  // N: output columns (I or H)
     int NT, KS, KC;                  // column tiles of a panel; k-steps and chunks
-    int act_KS, act_KC;              // of GEMM1's output rows
-    int max_mtiles;
+    int srow;                        // bytes of a row's scales
+    int act_KS, act_srow;            // of GEMM1's output rows
+    int max_mtiles;                  // upper bound of the M-tiles
+    int BM;                          // rows of an M-tile: 32, 64, 128 or 256
 };
 hipError_t launch_mx_gemm(bool g1, int bits, const MxGemmArgs &a, int num_cus, hipStream_t s);
 

@@ -27,17 +27,18 @@
 //
 // Packed weights of a stack [E, Kd, N] whose columns form `panels` equal
 // panels (up_proj: gate and up; down_proj: one), NT = ceil(N / panels / 32)
-// column tiles each, KS = ceil(Kd / 64) k-steps, KC = ceil(KS / 4) chunks:
+// column tiles each, KS = 2 ceil(Kd / 128) k-steps, KC = ceil(KS / 4) chunks:
 //   codes  [E][panels][NT][KS][64 lanes][16 bytes]
 //   scales [E][panels][NT][KC][64 lanes][4 k-steps]      (256-byte aligned)
 // so that one wave's operand of a k-step is 1024 contiguous bytes, straight
 // from memory into registers, and a column tile's whole contraction is one
-// contiguous stream.  Columns and k past the ends are zero.
+// contiguous stream.  Columns and k past the ends are zero (an even number of
+// k-steps: the tile kernel's loop takes them in pairs).
 //
 // Activations are row-major: the first 16 bytes of every block's codes
 // [rows][2 KS][16], for e2m3 the other 8 in an array of their own
 // [rows][2 KS][8] (both then load as whole vectors), and the scales
-// [rows][KC][2 k-blocks][4 k-steps].
+// [rows][KC rounded up to even][2 k-blocks][4 k-steps] (whole 16 bytes a row).
 #pragma once
 
 #include "common.h"
@@ -51,13 +52,13 @@ constexpr int kMxNan = 255;  // E8M0 code of NaN
 struct MxDims {
     int NT, KS, KC;
     __host__ __device__ MxDims(int64_t Kd, int64_t panel_cols)
-        : NT((int)((panel_cols + 31) / 32)), KS((int)((Kd + 63) / 64)), KC((KS + 3) / 4)
+        : NT((int)((panel_cols + 31) / 32)), KS((int)((Kd + 127) / 128) * 2), KC((KS + 3) / 4)
     {
     }
     // bytes of an activation row: first 16 and last 8 bytes of the blocks, scales
     __host__ __device__ int code_row() const { return KS * 32; }
     __host__ __device__ int tail_row(int bits) const { return bits == 6 ? KS * 16 : 0; }
-    __host__ __device__ int scale_row() const { return KC * 8; }
+    __host__ __device__ int scale_row() const { return (KC + 1) / 2 * 16; }
 };
 
 // place of k-block b's scale byte in an activation row's scales

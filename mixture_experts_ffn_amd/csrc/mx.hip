@@ -99,7 +99,7 @@ __global__ __launch_bounds__(256) void mx_dequantize_weight_kernel(
 template <int BITS>
 __global__ __launch_bounds__(256) void mx_quantize_rows_kernel(
     const bf16 *__restrict__ x, u32x4 *__restrict__ codes, u32x2 *__restrict__ tails,
-    uint8_t *__restrict__ scales, int64_t T, int H, int KS, int KC)
+    uint8_t *__restrict__ scales, int64_t T, int H, int KS, int srow)
 {
     const int64_t n = T * (2 * KS);
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n;
@@ -133,7 +133,7 @@ __global__ __launch_bounds__(256) void mx_quantize_rows_kernel(
             codes[i] = u32x4{c[0], c[1], c[2], c[3]};
             tails[i] = u32x2{c[4], c[5]};
         }
-        scales[t * (KC * 8) + mx_scale_at(b)] = (uint8_t)code;
+        scales[t * srow + mx_scale_at(b)] = (uint8_t)code;
     }
 }
 
@@ -179,7 +179,7 @@ hipError_t launch_mx_quantize_rows(int bits, const void *x, void *codes, void *t
     auto k = bits == 4 ? mx_quantize_rows_kernel<4> : mx_quantize_rows_kernel<6>;
     hipLaunchKernelGGL(k, grid, dim3(256), 0, s, static_cast<const bf16 *>(x),
                        static_cast<u32x4 *>(codes), static_cast<u32x2 *>(tails),
-                       static_cast<uint8_t *>(scales), T, (int)H, d.KS, d.KC);
+                       static_cast<uint8_t *>(scales), T, (int)H, d.KS, d.scale_row());
     return hipGetLastError();
 }
 
