@@ -1356,7 +1356,7 @@ struct MxFwdLayout {
 int mx_tile_rows(const moe_ffn_problem &p)
 {
     const double rows = (double)(p.T * p.K) / (double)p.E;
-    return rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 1024 ? 128 : 256;
+    return rows <= 20 ? 32 : rows <= 44 ? 64 : rows <= 1024 ? 128 : 256;
 }
 
 MxFwdLayout mx_fwd_layout(const moe_ffn_problem &p, int bits)
@@ -1405,6 +1405,8 @@ int validate_mx_fwd(const moe_ffn_problem *p, int32_t act_format, uint32_t flags
         return fail(MOE_FFN_ERR_DTYPE, "act_format must be MXFP4 or MXFP6 (got %d)", act_format);
     if (p->Is != 0)
         return fail(MOE_FFN_ERR_SHAPE, "the MXFP4 forward takes no shared expert (Is must be 0)");
+    if (p->T * moe::MxDims(p->H, p->I).code_row() >= (int64_t(1) << 32))
+        return fail(MOE_FFN_ERR_SHAPE, "T*H must be < 2^33 (4 GiB of quantised tokens)");
     if (flags & ~(MOE_FFN_CHECK_IDS | MOE_FFN_CHECK_STATUS))
         return fail(MOE_FFN_ERR_SHAPE, "flags: only CHECK_IDS and CHECK_STATUS apply (got 0x%x)",
                     flags);
@@ -1538,6 +1540,7 @@ int moe_ffn_mxfp4_fwd(const moe_ffn_problem *p, int32_t act_format, const void *
     g.mtile_expert = rb.mtile_expert;
     g.max_mtiles = (int)L.max_mtiles;
     g.E = E;
+    g.T = p->T;
     g.topk = (int)p->K;
     g.act_codes = at<uint8_t>(ws, L.act_codes);
     g.act_tails = at<uint8_t>(ws, L.act_tails);

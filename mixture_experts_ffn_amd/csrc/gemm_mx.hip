@@ -126,75 +126,165 @@ template <int BITS> __device__ inline void store_empty(const ActRow &r, int bloc
     }
 }
 
+// `n` bytes from p as a buffer: loads take a scalar base, a scalar offset and
+// one register of lane offset, and past the end they return zero.
+__device__ inline __amdgpu_buffer_rsrc_t bytes_at(const void *p, uint32_t n)
+{
+    const uint64_t b = (uint64_t)(uintptr_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc((void *)(uintptr_t)((uint64_t)hi << 32 | lo), 0,
+                                             __builtin_amdgcn_readfirstlane(n), 0x00020000);
+}
+
+// The token operand of a tile of rows r0 .. r0 + nr - 1: GEMM1 gathers rows of
+// x (all of them within 4 GiB of codes, which the host checks), GEMM2 reads
+// consecutive rows of act.
+struct TokenRows {
+    __amdgpu_buffer_rsrc_t codes, tails, scales;
+};
+template <int BITS, bool G1>
+__device__ inline TokenRows token_rows(const MxGemmArgs &a, int64_t r0, int64_t nr)
+{
+    const int64_t first = G1 ? 0 : r0, n = G1 ? a.T : nr;
+    TokenRows t;
+    t.codes = bytes_at(a.acodes + first * (a.KS * 32), (uint32_t)(n * (a.KS * 32)));
+    t.tails = t.codes;
+    if constexpr (BITS == 6)
+        t.tails = bytes_at(a.atails + first * (a.KS * 16), (uint32_t)(n * (a.KS * 16)));
+    t.scales = bytes_at(a.ascales + first * a.srow, (uint32_t)(n * a.srow));
+    return t;
+}
+
 // Weight streaming kernel.  A tile is 32 token rows of one expert times four
 // column tiles (GEMM1: two gate and the same two up tiles); the four waves
 // split the contraction, each streaming its part of the weights from memory
-// straight into registers, and are summed through LDS at the end.
+// straight into registers, and are summed through LDS at the end.  What a wave
+// needs is in flight two k-steps (8 KB of weights) ahead, across the end of a
+// tile too: the next tile's first steps are requested before this tile's sums
+// are joined.
+template <int BITS> struct StreamPair {
+    u32x4 w[4][2]; // [tile][k-step]
+    MxFrag<BITS> a[2];
+};
+struct StreamScales {
+    int w[4], a;
+};
+
 template <int BITS, bool G1>
 __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxGemmArgs a)
 {
+    using namespace tile;
     __shared__ f32x4 red[4][3][4][64]; // [tile][other wave][register / 4][lane]
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = uni(threadIdx.x >> 6);
     const int h = lane >> 5;
     constexpr int PER = G1 ? 2 : 4; // column tiles of a panel
     const int ncg = (a.NT + PER - 1) / PER;
-    const int64_t total = (int64_t)a.mtile_off[a.E] * ncg;
+    const int64_t total = (int64_t)ldc(a.mtile_off, a.E) * ncg;
     // an XCD's workgroups (blockIdx % 8) take a contiguous part of the tiles,
     // so an expert's token rows stay in one L2
     const int xcd = blockIdx.x & 7;
     const int64_t t1 = total * (xcd + 1) / 8;
-    for (int64_t t = total * xcd / 8 + (blockIdx.x >> 3); t < t1; t += gridDim.x >> 3) {
-        const int m = (int)(t / ncg), cg = (int)(t - (int64_t)m * ncg);
-        const int e = a.mtile_expert[m];
-        const int r0 = a.offsets[e] + (m - a.mtile_off[e]) * 32;
-        const int nr = min(32, a.offsets[e + 1] - r0);
-        const int row = r0 + min(lane & 31, nr - 1);
-        const int64_t arow = G1 ? a.sorted_slot[row] / a.topk : row;
-        const uint8_t *ac = a.acodes + arow * (a.KS * 32) + h * 16;
-        const uint8_t *at = BITS == 6 ? a.atails + arow * (a.KS * 16) + h * 8 : nullptr;
-        const uint8_t *as = a.ascales + arow * a.srow + h * 4;
-        const uint8_t *wc[4], *ws[4];
+    // the wave's k-step pairs [p0, p1): whole chunks, the last one may be half
+    const int p0 = a.KC * wave / 4 * 2, p1 = min(a.KC * (wave + 1) / 4 * 2, a.KS >> 1);
+
+    struct Place {
+        int cg, nr, row;
+        uint32_t ao, so;                       // this lane's token row: codes, scales
+        __amdgpu_buffer_rsrc_t ac, at, as;     // token rows
+        __amdgpu_buffer_rsrc_t wc, ws;         // the expert's weights
+        int tile[4];                           // column tiles, counted from there
+    };
+    auto place = [&](int64_t t, Place &q) {
+        const int m = (int)(t / ncg);
+        q.cg = uni((int)(t - (int64_t)m * ncg));
+        const int e = ldc(a.mtile_expert, m);
+        const int r0 = ldc(a.offsets, e) + (m - ldc(a.mtile_off, e)) * 32;
+        q.nr = min(32, ldc(a.offsets, e + 1) - r0);
+        const int r = min(lane & 31, q.nr - 1);
+        q.row = r0 + r;
+        const TokenRows tr = token_rows<BITS, G1>(a, r0, q.nr);
+        q.ac = tr.codes;
+        q.at = tr.tails;
+        q.as = tr.scales;
+        const uint32_t arow = G1 ? a.sorted_slot[q.row] / a.topk : r;
+        q.ao = arow * (uint32_t)(a.KS * 32) + h * 16;
+        q.so = arow * (uint32_t)a.srow + h * 4;
+        const int64_t tiles = (int64_t)a.NT * (G1 ? 2 : 1); // of an expert
+        q.wc = bytes_at(a.wcodes + e * tiles * a.KS * 1024, (uint32_t)(tiles * a.KS * 1024));
+        q.ws = bytes_at(a.wscales + e * tiles * a.KC * 256, (uint32_t)(tiles * a.KC * 256));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c = min(cg * PER + (G1 ? j >> 1 : j), a.NT - 1);
-            const int64_t tile = ((int64_t)e * (G1 ? 2 : 1) + (G1 ? j & 1 : 0)) * a.NT + c;
-            wc[j] = a.wcodes + tile * a.KS * 1024 + lane * 16;
-            ws[j] = a.wscales + tile * a.KC * 256 + lane * 4;
+        for (int j = 0; j < 4; ++j)
+            q.tile[j] = min(q.cg * PER + (G1 ? j >> 1 : j), a.NT - 1) + (G1 ? (j & 1) * a.NT : 0);
+    };
+    const uint32_t wl = lane * 16, sl = lane * 4;
+    auto load = [&](const Place &q, int p, StreamPair<BITS> &x) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            x.a[s].c = __builtin_amdgcn_raw_buffer_load_b128(q.ac, q.ao + s * 32, p * 64, 0);
+            if constexpr (BITS == 6)
+                x.a[s].t = __builtin_amdgcn_raw_buffer_load_b64(q.at, (q.ao >> 1) + s * 16, p * 32, 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                x.w[j][s] = __builtin_amdgcn_raw_buffer_load_b128(
+                    q.wc, wl + s * 1024, q.tile[j] * a.KS * 1024 + p * 2048, 0);
         }
-        f32x16 acc[4];
+    };
+    auto load_scales = [&](const Place &q, int kc, StreamScales &x) {
+        x.a = __builtin_amdgcn_raw_buffer_load_b32(q.as, q.so, kc * 8, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            x.w[j] = __builtin_amdgcn_raw_buffer_load_b32(q.ws, sl, (q.tile[j] * a.KC + kc) * 256, 0);
+    };
+    f32x16 acc[4];
+    auto compute = [&](const StreamPair<BITS> &x, const StreamScales &sc, auto ODD) {
+        constexpr int s = 2 * decltype(ODD)::value;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc[j] = mx_mma<BITS, s>(x.w[j][0], sc.w[j], x.a[0], sc.a, acc[j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc[j] = mx_mma<BITS, s + 1>(x.w[j][1], sc.w[j], x.a[1], sc.a, acc[j]);
+    };
+
+    int64_t t = total * xcd / 8 + (blockIdx.x >> 3);
+    if (t >= t1)
+        return;
+    Place q;
+    StreamPair<BITS> x, y;
+    StreamScales sc, next;
+    auto first = [&] {
+        place(t, q);
+        if (p0 < p1) {
+            load_scales(q, p0 >> 1, next);
+            load(q, p0, x);
+        }
+    };
+    first();
+    while (true) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 acc[j][i] = 0.f;
-        const int c0 = a.KC * wave / 4, c1 = a.KC * (wave + 1) / 4;
-        for (int kc = c0; kc < c1; ++kc) {
-            int wsc[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                wsc[j] = *reinterpret_cast<const int *>(ws[j] + (int64_t)kc * 256);
-            const int asc = *reinterpret_cast<const int *>(as + kc * 8);
-            auto step = [&](auto S) {
-                constexpr int s = decltype(S)::value;
-                const int ks = kc * 4 + s;
-                if (ks >= a.KS)
-                    return;
-                MxFrag<BITS> av;
-                av.c = *reinterpret_cast<const u32x4 *>(ac + ks * 32);
-                if constexpr (BITS == 6)
-                    av.t = *reinterpret_cast<const u32x2 *>(at + ks * 16);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const u32x4 w = *reinterpret_cast<const u32x4 *>(wc[j] + (int64_t)ks * 1024);
-                    acc[j] = mx_mma<BITS, s>(w, wsc[j], av, asc, acc[j]);
+        for (int p = p0; p < p1; p += 2) {
+            sc = next;
+            if (p + 1 < p1)
+                load(q, p + 1, y);
+            compute(x, sc, IC<0>{});
+            if (p + 1 < p1) {
+                if (p + 2 < p1) {
+                    load_scales(q, (p >> 1) + 1, next);
+                    load(q, p + 2, x);
                 }
-            };
-            step(std::integral_constant<int, 0>{});
-            step(std::integral_constant<int, 1>{});
-            step(std::integral_constant<int, 2>{});
-            step(std::integral_constant<int, 3>{});
+                compute(y, sc, IC<1>{});
+            }
         }
+        const int cg = q.cg, nr = q.nr, row = q.row;
+        t += gridDim.x >> 3;
+        if (t < t1)
+            first();
         // wave w sums tile w
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -259,6 +349,8 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxGemmArgs a)
                 }
             }
         }
+        if (t >= t1)
+            return;
         __syncthreads();
     }
 }
@@ -270,7 +362,7 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxGemmArgs a)
 // which all four waves read, are copied into a ring of LDS stages of two
 // k-steps, 64 bytes of codes a row, swizzled like the bf16 kernels' rows.
 template <int BITS, bool G1, int TF>
-__global__ __launch_bounds__(256, TF == 8 ? 1 : 2) void mx_tile_kernel(MxGemmArgs a)
+__global__ __launch_bounds__(256, TF == 8 ? 1 : TF == 4 ? 2 : 3) void mx_tile_kernel(MxGemmArgs a)
 {
     using namespace tile;
     constexpr int ROWS = TF * 32;
@@ -281,9 +373,7 @@ __global__ __launch_bounds__(256, TF == 8 ? 1 : 2) void mx_tile_kernel(MxGemmArg
     constexpr int NL = 4;                            // weight loads of a wave and stage
     __shared__ __attribute__((aligned(1024))) unsigned char smem[RING * STAGE + 2 * SCALES];
     unsigned char *const sscale = smem + RING * STAGE;
-    const int lane = threadIdx.x & 63;
     const int wave = uni(threadIdx.x >> 6);
-    const int h = lane >> 5, fr = lane & 31;
     constexpr int PER = G1 ? 4 : 8; // column tiles of a panel
     const int ncg = (a.NT + PER - 1) / PER;
     const int KP = a.KS >> 1; // stages
@@ -291,6 +381,11 @@ __global__ __launch_bounds__(256, TF == 8 ? 1 : 2) void mx_tile_kernel(MxGemmArg
     const int xcd = blockIdx.x & 7;
     const int64_t t1 = total * (xcd + 1) / 8;
     for (int64_t t = total * xcd / 8 + (blockIdx.x >> 3); t < t1; t += gridDim.x >> 3) {
+        // what depends on the lane alone is formed anew for each tile: kept
+        // across the tiles it would not fit beside the accumulators
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));
+        const int h = lane >> 5, fr = lane & 31;
         // expert-major; inside an expert groups of up to 8 M-tiles, column
         // groups outer and M-tiles inner, so that tiles in flight share weights
         const int e = ldc(a.mtile_expert, (int)(t / ncg));
@@ -304,31 +399,36 @@ __global__ __launch_bounds__(256, TF == 8 ? 1 : 2) void mx_tile_kernel(MxGemmArg
         const int r0 = ldc(a.offsets, e) + mt * ROWS;
         const int nr = min(ROWS, ldc(a.offsets, e + 1) - r0);
 
-        auto row_of = [&](int r) -> int64_t {
-            const int p = r0 + min(r, nr - 1);
-            return G1 ? a.sorted_slot[p] / a.topk : p;
+        // a copy moves 1024 bytes: 16 rows of codes, 32 of tails, 64 of scales.
+        // Byte offsets of this lane's sources from a scalar base (GEMM1: the
+        // whole of x's codes, below 4 GiB; GEMM2: the tile's first row).
+        const int64_t first = G1 ? 0 : r0;
+        auto row_of = [&](int r) -> uint32_t {
+            r = min(r, nr - 1);
+            return G1 ? a.sorted_slot[r0 + r] / a.topk : r;
         };
-        // a copy moves 1024 bytes: 16 rows of codes, 32 of tails, 64 of scales
-        const uint8_t *src_c[NC], *src_t[NTL + 1], *src_s;
+        const uint8_t *const bc = a.acodes + first * (a.KS * 32);
+        const uint8_t *const bt = BITS == 6 ? a.atails + first * (a.KS * 16) : nullptr;
+        const uint8_t *const bs = a.ascales + first * a.srow;
+        uint32_t src_c[NC], src_t[NTL + 1], src_s;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int r = (wave * NC + i) * 16 + (lane >> 2);
-            src_c[i] = a.acodes + row_of(r) * (a.KS * 32) + aswz<4>(r, lane & 3) * 16;
+            src_c[i] = row_of(r) * (uint32_t)(a.KS * 32) + aswz<4>(r, lane & 3) * 16;
         }
 #pragma unroll
         for (int i = 0; i < NTL; ++i) {
             const int r = ((wave * NTL + i) * 32 + (lane >> 1)) & (ROWS - 1);
-            src_t[i] = a.atails + row_of(r) * (a.KS * 16) + (lane & 1) * 16;
+            src_t[i] = row_of(r) * (uint32_t)(a.KS * 16) + (lane & 1) * 16;
         }
-        src_s = a.ascales + row_of((wave * 64 + lane) & (ROWS - 1)) * a.srow;
-        const uint8_t *wc[2], *ws[2];
+        src_s = row_of((wave * 64 + lane) & (ROWS - 1)) * (uint32_t)a.srow;
+        const int64_t tiles = (int64_t)a.NT * (G1 ? 2 : 1); // of an expert
+        const auto wc = bytes_at(a.wcodes + e * tiles * a.KS * 1024, (uint32_t)(tiles * a.KS * 1024));
+        const auto ws = bytes_at(a.wscales + e * tiles * a.KC * 256, (uint32_t)(tiles * a.KC * 256));
+        int tl[2]; // the wave's column tiles
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int c = min(cg * PER + (G1 ? wave : 2 * wave + j), a.NT - 1);
-            const int64_t tile = ((int64_t)e * (G1 ? 2 : 1) + (G1 ? j : 0)) * a.NT + c;
-            wc[j] = a.wcodes + tile * a.KS * 1024;
-            ws[j] = a.wscales + tile * a.KC * 256;
-        }
+        for (int j = 0; j < 2; ++j)
+            tl[j] = uni(min(cg * PER + (G1 ? wave : 2 * wave + j), a.NT - 1) + (G1 ? j * a.NT : 0));
         const uint32_t wl = lane * 16, sl = lane * 4;
         // copies of stage p (past the end: of the last one, into a stage that is not read again)
         auto copy = [&](int p) {
@@ -336,36 +436,38 @@ __global__ __launch_bounds__(256, TF == 8 ? 1 : 2) void mx_tile_kernel(MxGemmArg
             const int q = min(p, KP - 1);
 #pragma unroll
             for (int i = 0; i < NC; ++i)
-                g2l16(src_c[i] + q * 64, (lds_void *)(st + (wave * NC + i) * 1024));
+                g2l16s(bc + q * 64, src_c[i], (lds_void *)(st + (wave * NC + i) * 1024));
 #pragma unroll
             for (int i = 0; i < NTL; ++i)
                 if (TF >= 4 || wave < 2)
-                    g2l16(src_t[i] + q * 32, (lds_void *)(st + CODES + (wave * NTL + i) * 1024));
+                    g2l16s(bt + q * 32, src_t[i],
+                           (lds_void *)(st + CODES + (wave * NTL + i) * 1024));
         };
         // scales of the four stages 4g .. 4g + 3
         auto copy_scales = [&](int g) {
             if (wave < TF / 2)
-                g2l16(src_s + g * 16, (lds_void *)(sscale + (g & 1) * SCALES + wave * 1024));
+                g2l16s(bs + g * 16, src_s, (lds_void *)(sscale + (g & 1) * SCALES + wave * 1024));
         };
         struct W {
             u32x4 c[2][2];
         };
         auto load_w = [&](int p, W &w) {
-            const int64_t at = (int64_t)min(p, KP - 1) * 2048;
+            const int q = min(p, KP - 1) * 2;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
-                    w.c[j][s] = *reinterpret_cast<const u32x4 *>(wc[j] + at + s * 1024 + wl);
+                    w.c[j][s] = __builtin_amdgcn_raw_buffer_load_b128(
+                        wc, wl + s * 1024, (tl[j] * a.KS + q) * 1024, 0);
         };
         struct S {
             int w[2];
         };
         auto load_s = [&](int kc, S &s) {
-            const int64_t at = (int64_t)min(kc, a.KC - 1) * 256;
+            const int q = min(kc, a.KC - 1);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                s.w[j] = *reinterpret_cast<const int *>(ws[j] + at + sl);
+                s.w[j] = __builtin_amdgcn_raw_buffer_load_b32(ws, sl, (tl[j] * a.KC + q) * 256, 0);
         };
         f32x16 acc[2][TF];
 #pragma unroll
@@ -487,7 +589,7 @@ hipError_t launch_mx_gemm(bool g1, int bits, const MxGemmArgs &a, int num_cus, h
     const bool stream = a.BM == 32;
     const int per = stream ? (g1 ? 2 : 4) : (g1 ? 4 : 8);
     const int64_t most = (int64_t)a.max_mtiles * ((a.NT + per - 1) / per);
-    int64_t grid = (int64_t)num_cus * (stream ? 16 : a.BM == 256 ? 1 : 2);
+    int64_t grid = (int64_t)num_cus * (a.BM == 256 ? 1 : a.BM == 64 ? 3 : 2);
     if (most < grid)
         grid = most;
     grid = (grid + 7) / 8 * 8; // a whole number of workgroups for each XCD

@@ -219,6 +219,7 @@ struct MxGemmArgs {
     const int32_t *offsets;          // [E + 1]
     const int32_t *mtile_off;        // [E + 1]
     const int32_t *mtile_expert;     // [max_mtiles]
+    int64_t T;                       // tokens
     int E, topk, N;                  // N: output columns (I or H)
     int NT, KS, KC;                  // column tiles of a panel; k-steps and chunks
     int srow;                        // bytes of a row's scales
