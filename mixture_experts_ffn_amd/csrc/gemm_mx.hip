@@ -355,17 +355,17 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxGemmArgs a)
     }
 }
 
-// Tile kernel.  A tile is 32 TF token rows of one expert times eight column
-// tiles, two a wave: GEMM1 a gate tile and the up tile of the same columns (so
+// Tile kernel.  A tile is 32 TF WR token rows of one expert times eight column
+// tiles; a wave has 32 TF rows of two of them: GEMM1 a gate tile and the up tile of the same columns (so
 // the epilogue stays in the wave), GEMM2 two neighbours.  The weights go from
 // memory straight into registers, since the waves share none; the token rows,
 // which all four waves read, are copied into a ring of LDS stages of two
 // k-steps, 64 bytes of codes a row, swizzled like the bf16 kernels' rows.
-template <int BITS, bool G1, int TF>
-__global__ __launch_bounds__(256, TF == 8 ? 1 : TF == 4 ? 2 : 3) void mx_tile_kernel(MxGemmArgs a)
+template <int BITS, bool G1, int TF, int WR>
+__global__ __launch_bounds__(256 * WR, TF == 4 ? 2 : 3) void mx_tile_kernel(MxGemmArgs a)
 {
     using namespace tile;
-    constexpr int ROWS = TF * 32;
+    constexpr int ROWS = WR * TF * 32;
     constexpr int CODES = ROWS * 64, TAILS = BITS == 6 ? ROWS * 32 : 0, SCALES = ROWS * 16;
     constexpr int STAGE = CODES + TAILS, RING = 4;
     constexpr int NC = TF / 2;                       // code copies of a wave and stage
@@ -374,6 +374,7 @@ __global__ __launch_bounds__(256, TF == 8 ? 1 : TF == 4 ? 2 : 3) void mx_tile_ke
     __shared__ __attribute__((aligned(1024))) unsigned char smem[RING * STAGE + 2 * SCALES];
     unsigned char *const sscale = smem + RING * STAGE;
     const int wave = uni(threadIdx.x >> 6);
+    const int wr = wave >> 2, wn = wave & 3; // wave row, wave column
     constexpr int PER = G1 ? 4 : 8; // column tiles of a panel
     const int ncg = (a.NT + PER - 1) / PER;
     const int KP = a.KS >> 1; // stages
@@ -386,6 +387,7 @@ __global__ __launch_bounds__(256, TF == 8 ? 1 : TF == 4 ? 2 : 3) void mx_tile_ke
         int lane = threadIdx.x & 63;
         asm volatile("" : "+v"(lane));
         const int h = lane >> 5, fr = lane & 31;
+        const int row0 = wr * (TF * 32); // this wave's rows of the tile
         // expert-major; inside an expert groups of up to 8 M-tiles, column
         // groups outer and M-tiles inner, so that tiles in flight share weights
         const int e = ldc(a.mtile_expert, (int)(t / ncg));
@@ -428,7 +430,7 @@ __global__ __launch_bounds__(256, TF == 8 ? 1 : TF == 4 ? 2 : 3) void mx_tile_ke
         int tl[2]; // the wave's column tiles
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            tl[j] = uni(min(cg * PER + (G1 ? wave : 2 * wave + j), a.NT - 1) + (G1 ? j * a.NT : 0));
+            tl[j] = uni(min(cg * PER + (G1 ? wn : 2 * wn + j), a.NT - 1) + (G1 ? j * a.NT : 0));
         const uint32_t wl = lane * 16, sl = lane * 4;
         // copies of stage p (past the end: of the last one, into a stage that is not read again)
         auto copy = [&](int p) {
@@ -445,7 +447,7 @@ __global__ __launch_bounds__(256, TF == 8 ? 1 : TF == 4 ? 2 : 3) void mx_tile_ke
         };
         // scales of the four stages 4g .. 4g + 3
         auto copy_scales = [&](int g) {
-            if (wave < TF / 2)
+            if (wave < ROWS / 64)
                 g2l16s(bs + g * 16, src_s, (lds_void *)(sscale + (g & 1) * SCALES + wave * 1024));
         };
         struct W {
@@ -484,13 +486,13 @@ __global__ __launch_bounds__(256, TF == 8 ? 1 : TF == 4 ? 2 : 3) void mx_tile_ke
             int as[TF];
 #pragma unroll
             for (int f = 0; f < TF; ++f)
-                as[f] = *reinterpret_cast<const int *>(sc + (f * 32 + fr) * 16);
+                as[f] = *reinterpret_cast<const int *>(sc + (row0 + f * 32 + fr) * 16);
             auto step = [&](auto H) {
                 constexpr int s = decltype(H)::value;
                 constexpr int sel = 2 * decltype(ODD)::value + s;
 #pragma unroll
                 for (int f = 0; f < TF; ++f) {
-                    const int r = f * 32 + fr;
+                    const int r = row0 + f * 32 + fr;
                     MxFrag<BITS> av;
                     av.c = *reinterpret_cast<const u32x4 *>(st + r * 64 + aswz<4>(r, 2 * s + h) * 16);
                     if constexpr (BITS == 6)
@@ -540,10 +542,10 @@ __global__ __launch_bounds__(256, TF == 8 ? 1 : TF == 4 ? 2 : 3) void mx_tile_ke
         lds_barrier();
         // the last barrier: every wave is past its reads, so the next tile may copy
         if constexpr (G1) {
-            const int c = cg * 4 + wave;
+            const int c = cg * 4 + wn;
 #pragma unroll
             for (int f = 0; f < TF; ++f) {
-                const int r = f * 32 + fr;
+                const int r = row0 + f * 32 + fr;
                 const bool live = r < nr && c < a.NT;
                 const ActRow ar = act_row<BITS>(a, r0 + min(r, nr - 1));
                 store_act<BITS>(acc[0][f], acc[1][f], ar, c, live);
@@ -553,10 +555,10 @@ __global__ __launch_bounds__(256, TF == 8 ? 1 : TF == 4 ? 2 : 3) void mx_tile_ke
         } else {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int col = (cg * 8 + 2 * wave + j) * 32 + 16 * h;
+                const int col = (cg * 8 + 2 * wn + j) * 32 + 16 * h;
 #pragma unroll
                 for (int f = 0; f < TF; ++f) {
-                    const int r = f * 32 + fr;
+                    const int r = row0 + f * 32 + fr;
                     float v[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
@@ -579,9 +581,9 @@ __global__ __launch_bounds__(256, TF == 8 ? 1 : TF == 4 ? 2 : 3) void mx_tile_ke
 
 template <int BITS, bool G1> static auto tile_kernel(int BM)
 {
-    return BM == 64 ? mx_tile_kernel<BITS, G1, 2>
-           : BM == 128 ? mx_tile_kernel<BITS, G1, 4>
-                       : mx_tile_kernel<BITS, G1, 8>;
+    return BM == 64    ? mx_tile_kernel<BITS, G1, 2, 1>
+           : BM == 128 ? mx_tile_kernel<BITS, G1, 4, 1>
+                       : mx_tile_kernel<BITS, G1, 4, 2>;
 }
 
 hipError_t launch_mx_gemm(bool g1, int bits, const MxGemmArgs &a, int num_cus, hipStream_t s)
@@ -597,7 +599,7 @@ hipError_t launch_mx_gemm(bool g1, int bits, const MxGemmArgs &a, int num_cus, h
                           : (bits == 4 ? mx_stream_kernel<4, false> : mx_stream_kernel<6, false>))
              : g1   ? (bits == 4 ? tile_kernel<4, true>(a.BM) : tile_kernel<6, true>(a.BM))
                     : (bits == 4 ? tile_kernel<4, false>(a.BM) : tile_kernel<6, false>(a.BM));
-    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(a.BM == 256 ? 512 : 256), 0, s, a);
     return hipGetLastError();
 }
 
