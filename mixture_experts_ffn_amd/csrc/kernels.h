@@ -241,6 +241,11 @@ struct RouterArgs {
     int E, K, groups, topk_groups, group_top;
     bool bf16, ids64, sigmoid, renorm;
     float scale;
+    // set by the launches
+    bool vec, vec_out;    // rows start at multiples of 16 bytes
+    bool need_total;      // forward: the softmax denominator is used
+    int group_lanes;      // lanes that scan a group, a power of two
+    uint32_t group_m;     // expert / (E / groups) by multiplication
 };
 hipError_t launch_router_fwd(const RouterArgs &a, hipStream_t s);
 hipError_t launch_router_bwd(const RouterArgs &a, hipStream_t s);
