@@ -242,9 +242,10 @@ struct RouterArgs {
     bool bf16, ids64, sigmoid, renorm;
     float scale;
     // set by the launches
-    bool vec, vec_out;    // rows start at multiples of 16 bytes
+    bool vec, vec_out, vec_bias; // rows (and the bias) start at multiples of 16 bytes
     bool need_total;      // forward: the softmax denominator is used
     int group_lanes;      // lanes that scan a group, a power of two
+    int group_shift;      // sixteen lanes a row: log2 of a group's lanes
     uint32_t group_m;     // expert / (E / groups) by multiplication
 };
 hipError_t launch_router_fwd(const RouterArgs &a, hipStream_t s);
