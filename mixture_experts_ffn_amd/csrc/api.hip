@@ -1509,9 +1509,6 @@ int moe_ffn_mxfp4_fwd(const moe_ffn_problem *p, int32_t act_format, const void *
     const int64_t TK = p->T * p->K;
     const int E = (int)p->E;
 
-    HIP_TRY(moe::launch_mx_quantize_rows(bits, x, at<void>(ws, L.x_codes), at<void>(ws, L.x_tails),
-                                         at<void>(ws, L.x_scales), p->T, p->H, s),
-            "token quantisation launch");
     moe::RouteBufs rb{};
     rb.status = at<int32_t>(ws, L.status);
     rb.hist = at<int32_t>(ws, L.hist);
@@ -1523,8 +1520,11 @@ int moe_ffn_mxfp4_fwd(const moe_ffn_problem *p, int32_t act_format, const void *
     rb.sorted_slot = at<int32_t>(ws, L.sorted_slot);
     rb.slot_pos = at<int32_t>(ws, L.slot_pos);
     rb.T = p->T;
-    HIP_TRY(moe::launch_route(topk_ids, p->ids_dtype == MOE_FFN_I64, TK, E, L.BM, L.rp, rb, s),
-            "route launch");
+    const moe::MxRows rows{x, at<void>(ws, L.x_codes), at<void>(ws, L.x_tails),
+                           at<void>(ws, L.x_scales), p->T, (int)p->H, L.x.KS, L.x.scale_row(), bits};
+    HIP_TRY(moe::launch_route(topk_ids, p->ids_dtype == MOE_FFN_I64, TK, E, L.BM, L.rp, rb, s,
+                              &rows),
+            "route and token quantisation launch");
     if (flags & MOE_FFN_CHECK_IDS) {
         int32_t st = 0;
         HIP_TRY(hipMemcpyAsync(&st, rb.status, sizeof st, hipMemcpyDeviceToHost, s), "status copy");

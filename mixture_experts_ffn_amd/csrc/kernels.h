@@ -73,9 +73,21 @@ struct RouteBufs {
 enum { MOE_DEV_BAD_ID = 1, MOE_DEV_TIMEOUT = 2, MOE_DEV_BAD_SAVED = 4, MOE_DEV_BAD_WS = 8 };
 
 
+// Token rows x [T, H] bf16 to be quantised to codes of `bits` (4 or 6) bits,
+// row-major (mx.h)
+struct MxRows {
+    const void *x;
+    void *codes, *tails, *scales; // tails: 6 bits only
+    int64_t T;
+    int H, KS, srow, bits;
+};
+
 RoutePlan make_route_plan(int64_t TK, int E);
+// rows: token rows that are quantised by further blocks of the routing launch
+// (or by a launch of their own where the routing takes three)
 hipError_t launch_route(const void *ids, bool ids64, int64_t TK, int E, int BM,
-                        const RoutePlan &rp, const RouteBufs &rb, hipStream_t stream);
+                        const RoutePlan &rp, const RouteBufs &rb, hipStream_t stream,
+                        const MxRows *rows = nullptr);
 
 // upper bound of sum_e ceil(counts[e] / BM) over any routing of TK slots
 inline int64_t max_mtiles_bound(int64_t TK, int E, int BM)
@@ -207,9 +219,7 @@ hipError_t launch_mx_quantize_weight(int dtype, const void *w, void *codes, void
                                      int64_t Kd, int64_t N, int panels, hipStream_t s);
 hipError_t launch_mx_dequantize_weight(int dtype, const void *codes, const void *scales, void *w,
                                        int64_t E, int64_t Kd, int64_t N, int panels, hipStream_t s);
-// x [T, H] bf16 -> codes of `bits` (4 or 6) bits and scales, row-major
-hipError_t launch_mx_quantize_rows(int bits, const void *x, void *codes, void *tails, void *scales,
-                                   int64_t T, int64_t H, hipStream_t s);
+hipError_t launch_mx_quantize_rows(const MxRows &rows, hipStream_t s);
 struct MxGemmArgs {
     const uint8_t *wcodes, *wscales; // packed weights (GEMM1: two panels)
     const uint8_t *acodes, *atails, *ascales; // GEMM1: token rows; GEMM2: act rows (permuted)

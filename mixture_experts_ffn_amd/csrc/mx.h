@@ -42,6 +42,7 @@
 #pragma once
 
 #include "common.h"
+#include "kernels.h"
 
 namespace moe {
 
@@ -125,6 +126,45 @@ __device__ inline float mx_fp4_value(uint32_t code)
     const float a = m < 2 ? 0.5f * m
                           : __uint_as_float((uint32_t)(((m >> 1) + 126) << 23 | (m & 1) << 22));
     return code & 8 ? -a : a;
+}
+
+// Block i of the token rows (block i % (2 KS) of row i / (2 KS)): a lane owns
+// it, so its maximum needs no other lane and its codes are whole vectors.  The
+// row is padded with zeros to whole k-steps.
+template <int BITS> __device__ inline void mx_quantize_block(const MxRows &r, int64_t i)
+{
+    const int64_t t = i / (2 * r.KS);
+    const int b = (int)(i - t * (2 * r.KS));
+    const bf16 *x = static_cast<const bf16 *>(r.x) + t * r.H + b * 32;
+    float v[32];
+    uint32_t top = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        u32x4 raw = {0u, 0u, 0u, 0u};
+        if (b * 32 + q * 8 < r.H) // H is a multiple of 8
+            raw = *reinterpret_cast<const u32x4 *>(x + q * 8);
+        const bf16 *vv = reinterpret_cast<const bf16 *>(&raw);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[q * 8 + j] = static_cast<float>(vv[j]);
+            top = max(top, abs_bits(v[q * 8 + j]));
+        }
+    }
+    const int code = mx_scale_code(top);
+    const float inv = mx_inverse(code);
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        v[j] *= inv;
+    u32x4 *codes = static_cast<u32x4 *>(r.codes);
+    if constexpr (BITS == 4) {
+        codes[i] = u32x4{mx_pack8_fp4(v), mx_pack8_fp4(v + 8), mx_pack8_fp4(v + 16),
+                         mx_pack8_fp4(v + 24)};
+    } else {
+        const u32x6 c = mx_pack_fp6<32>(v);
+        codes[i] = u32x4{c[0], c[1], c[2], c[3]};
+        static_cast<u32x2 *>(r.tails)[i] = u32x2{c[4], c[5]};
+    }
+    static_cast<uint8_t *>(r.scales)[t * r.srow + mx_scale_at(b)] = (uint8_t)code;
 }
 
 } // namespace moe

@@ -20,16 +20,18 @@ template <typename T> struct __attribute__((aligned(2 * sizeof(T)))) Pair {
     T v[2];
 };
 
-// Place of a lane: its columns (col, col + 1) of a panel, its k-block.
+// Place of a lane: its columns (col, col + 1) of a panel, its k-step.  Column
+// pairs of tiles run fastest in blockIdx.x, which alone carries large numbers.
 struct WeightPlace {
     int64_t ep;  // expert * panels + panel
     int col, ks; // ks >= KS: nothing to do
 };
-__device__ inline WeightPlace weight_place()
+__device__ inline WeightPlace weight_place(int NT)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    return {(int64_t)blockIdx.z, (int)blockIdx.x * 64 + (lane & 31) * 2,
-            (int)blockIdx.y * 4 + wave};
+    const uint32_t ntp = (uint32_t)(NT + 1) / 2;
+    const uint32_t kq = blockIdx.x / ntp, tp = blockIdx.x - kq * ntp;
+    return {(int64_t)blockIdx.y, (int)tp * 64 + (lane & 31) * 2, (int)kq * 4 + wave};
 }
 
 template <typename T>
@@ -37,7 +39,7 @@ __global__ __launch_bounds__(256) void mx_quantize_weight_kernel(
     const T *__restrict__ w, u32x4 *__restrict__ codes, uint8_t *__restrict__ scales, int Kd, int N,
     int panels, int NT, int KS, int KC)
 {
-    const WeightPlace q = weight_place();
+    const WeightPlace q = weight_place(NT);
     const int half = (threadIdx.x & 63) >> 5;
     const int tile = q.col >> 5;
     if (q.ks >= KS || tile >= NT)
@@ -88,7 +90,7 @@ __global__ __launch_bounds__(256) void mx_dequantize_weight_kernel(
     const u32x4 *__restrict__ codes, const uint8_t *__restrict__ scales, T *__restrict__ w, int Kd,
     int N, int panels, int NT, int KS, int KC)
 {
-    const WeightPlace q = weight_place();
+    const WeightPlace q = weight_place(NT);
     const int half = (threadIdx.x & 63) >> 5;
     const int tile = q.col >> 5;
     const int pc = N / panels;
@@ -117,48 +119,14 @@ __global__ __launch_bounds__(256) void mx_dequantize_weight_kernel(
     }
 }
 
-// Token rows x [T, H] bf16 -> row-major codes and scales.  A lane owns a block:
-// its maximum needs no other lane and its codes are whole vectors.  The row is
-// padded with zeros to whole k-steps.
+// Token rows by a launch of their own (they mostly ride in the routing launch).
 template <int BITS>
-__global__ __launch_bounds__(256) void mx_quantize_rows_kernel(
-    const bf16 *__restrict__ x, u32x4 *__restrict__ codes, u32x2 *__restrict__ tails,
-    uint8_t *__restrict__ scales, int64_t T, int H, int KS, int srow)
+__global__ __launch_bounds__(256) void mx_quantize_rows_kernel(MxRows r)
 {
-    const int64_t n = T * (2 * KS);
+    const int64_t n = r.T * (2 * r.KS);
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n;
-         i += (int64_t)gridDim.x * 256) {
-        const int64_t t = i / (2 * KS);
-        const int b = (int)(i - t * (2 * KS));
-        float v[32];
-        uint32_t top = 0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            u32x4 raw = {0u, 0u, 0u, 0u};
-            if (b * 32 + q * 8 < H) // H is a multiple of 8
-                raw = *reinterpret_cast<const u32x4 *>(x + t * H + b * 32 + q * 8);
-            const bf16 *vv = reinterpret_cast<const bf16 *>(&raw);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[q * 8 + j] = static_cast<float>(vv[j]);
-                top = max(top, abs_bits(v[q * 8 + j]));
-            }
-        }
-        const int code = mx_scale_code(top);
-        const float inv = mx_inverse(code);
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            v[j] *= inv;
-        if constexpr (BITS == 4) {
-            codes[i] = u32x4{mx_pack8_fp4(v), mx_pack8_fp4(v + 8), mx_pack8_fp4(v + 16),
-                             mx_pack8_fp4(v + 24)};
-        } else {
-            const u32x6 c = mx_pack_fp6<32>(v);
-            codes[i] = u32x4{c[0], c[1], c[2], c[3]};
-            tails[i] = u32x2{c[4], c[5]};
-        }
-        scales[t * srow + mx_scale_at(b)] = (uint8_t)code;
-    }
+         i += (int64_t)gridDim.x * 256)
+        mx_quantize_block<BITS>(r, i);
 }
 
 template <typename T>
@@ -166,8 +134,8 @@ static hipError_t weight_t(bool quantize, const void *src, void *codes, void *sc
                            int64_t E, int64_t Kd, int64_t N, int panels, hipStream_t s)
 {
     const MxDims d(Kd, N / panels);
-    // grid.z carries at most 65535 (expert, panel) pairs; E <= 1024, panels <= 2
-    const dim3 grid((unsigned)((d.NT + 1) / 2), (unsigned)((d.KS + 3) / 4), (unsigned)(E * panels));
+    // E * panels <= 2048; Kd * N < 2^31 keeps grid.x within 2^22
+    const dim3 grid((unsigned)((d.NT + 1) / 2) * (unsigned)((d.KS + 3) / 4), (unsigned)(E * panels));
     if (quantize)
         hipLaunchKernelGGL(mx_quantize_weight_kernel<T>, grid, dim3(256), 0, s,
                            static_cast<const T *>(src), static_cast<u32x4 *>(codes),
@@ -194,16 +162,12 @@ hipError_t launch_mx_dequantize_weight(int dtype, const void *codes, const void 
                       : weight_t<float>(false, nullptr, c, x, w, E, Kd, N, panels, s);
 }
 
-hipError_t launch_mx_quantize_rows(int bits, const void *x, void *codes, void *tails, void *scales,
-                                   int64_t T, int64_t H, hipStream_t s)
+hipError_t launch_mx_quantize_rows(const MxRows &r, hipStream_t s)
 {
-    const MxDims d(H, 32);
-    const int64_t blocks = (T * d.KS * 2 + 255) / 256;
+    const int64_t blocks = (r.T * r.KS * 2 + 255) / 256;
     const dim3 grid((unsigned)(blocks < 8192 ? blocks : 8192));
-    auto k = bits == 4 ? mx_quantize_rows_kernel<4> : mx_quantize_rows_kernel<6>;
-    hipLaunchKernelGGL(k, grid, dim3(256), 0, s, static_cast<const bf16 *>(x),
-                       static_cast<u32x4 *>(codes), static_cast<u32x2 *>(tails),
-                       static_cast<uint8_t *>(scales), T, (int)H, d.KS, d.scale_row());
+    auto k = r.bits == 4 ? mx_quantize_rows_kernel<4> : mx_quantize_rows_kernel<6>;
+    hipLaunchKernelGGL(k, grid, dim3(256), 0, s, r);
     return hipGetLastError();
 }
 

@@ -33,6 +33,7 @@
 // scatter run as three launches.
 #include "common.h"
 #include "kernels.h"
+#include "mx.h"
 
 namespace moe {
 
@@ -383,10 +384,14 @@ __global__ __launch_bounds__(64) void route_scatter_kernel(
 // per-(expert, chunk) bases; block 0 also publishes counts, offsets, the
 // M-tile tables and the status word.  LDS: tab[E][16], tot[E], bef[E] (and
 // aft[E] in ROUTE_SELF).
+// RIDE = 4 or 6: blocks from `nblk` on quantise token rows to that many bits
+// instead.  Routing leaves nearly all of the chip idle and the rows need nothing
+// of it, so the two take the time of the longer one and a launch less (one token
+// of 7168: QBOTH us, 128: ..).
 enum { ROUTE_ONE = 0, ROUTE_SELF = 1, ROUTE_HIST = 2 };
 constexpr int64_t kSelfCountSlots = 32768;
 
-template <typename Id, int MODE>
+template <typename Id, int MODE, int RIDE>
 __global__ __launch_bounds__(1024) void route_block_kernel(
     const Id *__restrict__ ids, int64_t TK, int E, int nbits, int RC, int NB, int BM,
     const int32_t *__restrict__ hist, const int32_t *__restrict__ bad,
@@ -394,8 +399,17 @@ __global__ __launch_bounds__(1024) void route_block_kernel(
     int32_t *__restrict__ mtile_expert, MTileTable2 t2, int32_t *__restrict__ status,
     int32_t *__restrict__ ctr, int nctr, SavedHeader *__restrict__ hdr, uint64_t problem_hash,
     uint64_t epoch, int nsh, int64_t T, int K, int32_t *__restrict__ sorted_slot,
-    int32_t *__restrict__ slot_pos)
+    int32_t *__restrict__ slot_pos, int nblk, MxRows rows)
 {
+    if constexpr (RIDE != 0) {
+        if ((int)blockIdx.x >= nblk) {
+            const int64_t n = rows.T * (2 * rows.KS);
+            const int64_t step = (int64_t)(gridDim.x - nblk) * 1024;
+            for (int64_t i = (int64_t)(blockIdx.x - nblk) * 1024 + threadIdx.x; i < n; i += step)
+                mx_quantize_block<RIDE>(rows, i);
+            return;
+        }
+    }
     extern __shared__ int32_t lds[];
     int32_t *tab = lds;         // [E][16]: chunk counts, then chunk bases
     int32_t *tot = tab + E * 16; // [E]: slots of expert e over all chunks
@@ -746,9 +760,16 @@ RoutePlan make_route_plan(int64_t TK, int E)
     return rp;
 }
 
+template <typename Id, int RIDE> static auto route_block(int mode)
+{
+    return mode == ROUTE_ONE    ? route_block_kernel<Id, ROUTE_ONE, RIDE>
+           : mode == ROUTE_SELF ? route_block_kernel<Id, ROUTE_SELF, RIDE>
+                                : route_block_kernel<Id, ROUTE_HIST, RIDE>;
+}
+
 template <typename Id>
-static void launch_route_t(const Id *ids, int64_t TK, int E, int BM, const RoutePlan &rp,
-                           const RouteBufs &rb, hipStream_t stream)
+static hipError_t launch_route_t(const Id *ids, int64_t TK, int E, int BM, const RoutePlan &rp,
+                           const RouteBufs &rb, hipStream_t stream, const MxRows *rows)
 {
     const size_t lds = sizeof(int32_t) * (size_t)E;
     const size_t lds_block = sizeof(int32_t) * (size_t)E * 18; // tab[E][16], tot[E], bef[E]
@@ -766,16 +787,23 @@ static void launch_route_t(const Id *ids, int64_t TK, int E, int BM, const Route
         if (mode == ROUTE_HIST)
             hipLaunchKernelGGL(route_hist_kernel<Id>, dim3(rp.NB), dim3(64), lds, stream, ids, TK, E,
                                rp.RC, rp.NB, rb.hist, rb.bad);
-        auto kern = mode == ROUTE_ONE    ? route_block_kernel<Id, ROUTE_ONE>
-                    : mode == ROUTE_SELF ? route_block_kernel<Id, ROUTE_SELF>
-                                         : route_block_kernel<Id, ROUTE_HIST>;
-        hipLaunchKernelGGL(kern, dim3(nblk), dim3(1024), mode == ROUTE_SELF ? lds_self : lds_block,
+        auto kern = !rows             ? route_block<Id, 0>(mode)
+                    : rows->bits == 4 ? route_block<Id, 4>(mode)
+                                      : route_block<Id, 6>(mode);
+        const int64_t ride = rows ? (rows->T * rows->KS * 2 + 1023) / 1024 : 0;
+        const unsigned grid = (unsigned)(nblk + (ride < 2048 ? ride : 2048));
+        hipLaunchKernelGGL(kern, dim3(grid), dim3(1024), mode == ROUTE_SELF ? lds_self : lds_block,
                            stream, ids, TK, E, rp.nbits, rp.RC, rp.NB, BM, rb.hist, rb.bad,
                            rb.counts, rb.offsets, rb.mtile_off, rb.mtile_expert, t2, rb.status,
                            rb.ctr,
                            nctr, rb.saved_hdr, rb.problem_hash, rb.epoch, rb.nshared, rb.T, K,
-                           rb.sorted_slot, rb.slot_pos);
-        return;
+                           rb.sorted_slot, rb.slot_pos, nblk, rows ? *rows : MxRows{});
+        return hipGetLastError();
+    }
+    if (rows) {
+        const hipError_t err = launch_mx_quantize_rows(*rows, stream);
+        if (err != hipSuccess)
+            return err;
     }
     // many experts (the block table would not fit), or no slots: hist, scan, scatter
     if (TK > 0)
@@ -790,19 +818,18 @@ static void launch_route_t(const Id *ids, int64_t TK, int E, int BM, const Route
         hipLaunchKernelGGL(route_scatter_kernel<Id>, dim3(rp.NB), dim3(64), lds, stream, ids, TK, E,
                            rp.nbits, rp.RC, rp.NB, rb.hist, rb.offsets, rb.sorted_slot,
                            rb.slot_pos);
+    return hipGetLastError();
 }
 
 // One launch up to 32768 slots (16 chunks: one block; more: self-counting
 // blocks), two (hist, block) beyond, three (hist, scan, scatter) when an
 // expert table of 18 x E words would not fit 64 KB.
 hipError_t launch_route(const void *ids, bool ids64, int64_t TK, int E, int BM,
-                        const RoutePlan &rp, const RouteBufs &rb, hipStream_t stream)
+                        const RoutePlan &rp, const RouteBufs &rb, hipStream_t stream,
+                        const MxRows *rows)
 {
-    if (ids64)
-        launch_route_t((const int64_t *)ids, TK, E, BM, rp, rb, stream);
-    else
-        launch_route_t((const int32_t *)ids, TK, E, BM, rp, rb, stream);
-    return hipGetLastError();
+    return ids64 ? launch_route_t((const int64_t *)ids, TK, E, BM, rp, rb, stream, rows)
+                 : launch_route_t((const int32_t *)ids, TK, E, BM, rp, rb, stream, rows);
 }
 
 } // namespace moe

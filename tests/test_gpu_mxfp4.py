@@ -74,6 +74,19 @@ def test_quantize_special_values(gpu_lib, dtype):
     np.testing.assert_array_equal(as_f64(q), ref)
 
 
+@pytest.mark.parametrize("shape,panels", [((1, 1 << 25, 8), 1), ((1, 8, 1 << 25), 2)], ids=str)
+def test_quantize_long_and_thin(gpu_lib, shape, panels):
+    say(f"[mxfp4] quantize {shape}")
+    grid = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, -.5, -1, -1.5, -2, -3, -4, -6], device="cuda",
+                        dtype=torch.bfloat16)
+    gen = torch.Generator("cuda").manual_seed(7)
+    w = grid[torch.randint(0, 15, shape, device="cuda", generator=gen, dtype=torch.int32)]
+    w[:, ::8] = 6  # every block's scale is 1, so every value is kept
+    q = gpu_lib.moe_ffn_mxfp4_dequantize(gpu_lib.moe_ffn_mxfp4_quantize(w, panels=panels))
+    torch.cuda.synchronize()
+    assert torch.equal(q, w)
+
+
 def test_quantize_past_32_bit_offsets(gpu_lib):
     E, Kd, N = 40, 4096, 16384  # 2.7e9 values
     say(f"[mxfp4] quantize {E}x{Kd}x{N}")
@@ -153,6 +166,15 @@ SHAPES = [
 def test_ffn_sizes(gpu_lib, shape, act):
     say(f"[mxfp4] ffn {shape} {act}")
     check(gpu_lib, make(*shape), act)
+
+
+@pytest.mark.parametrize("act", ["mxfp4", "mxfp6"])
+@pytest.mark.parametrize("shape", [(4100, 40, 32, 5, 3), (8200, 72, 24, 9, 5), (650, 64, 32, 1000, 2),
+                                   (9, 64, 32, 1024, 5)], ids=str)
+def test_ffn_every_way_of_routing(gpu_lib, shape, act):
+    """Slots over several blocks, counted ahead, and more experts than a block's table holds."""
+    say(f"[mxfp4] routing {shape} {act}")
+    check(gpu_lib, make(*shape, seed=9), act)
 
 
 @pytest.mark.parametrize("act", ["mxfp4", "mxfp6"])
