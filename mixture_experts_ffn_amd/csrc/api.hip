@@ -10,6 +10,7 @@
 // shows why per-call context must not live in the operator).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -1352,11 +1353,26 @@ struct MxFwdLayout {
     size_t x_codes, x_tails, x_scales, act_codes, act_tails, act_scales, o, total;
 };
 
-// Rows of an M-tile from the mean rows per expert.
+// Rows of an M-tile (MXFP4, GEMM1 + GEMM2 in us; the sides of each rule):
+//  - mean rows per expert up to 20: 32, which pads least (16 x 7168 x 2048, 32
+//    experts, top 8: 127 against 131 with 64; 64 tokens: 134 and 133);
+//  - few tiles of 32 rows in all: 32, where four waves share a tile's
+//    contraction and the chain of a lone tile is shortest (256 x 1024 x 512, 8
+//    experts, top 2: 10 against 13; 1472 such tiles: 13 and 14; 2304: 17 and 15);
+//  - up to 48 mean rows, most experts fit 64 (512 x 2048 x 1408, 64 experts,
+//    top 6: 64 us against 74 with 128; 600 tokens, 56 rows: 77 and 71), and up to
+//    8192 tiles of 32 there are too few of 128 to fill the chip (1024 x 4096 x
+//    1536, 1 expert: 27 against 35; 4096 x 1024 x 1024, 2 experts, top 2: 32 and
+//    29);
+//  - else 128 (256 rows by eight waves: 1028 + 671 us against 1042 + 697 for the
+//    skewed workload with uniform routing, but 411 and 375 for 8192 x 4096 x
+//    1536, 16 experts, top 4).
 int mx_tile_rows(const moe_ffn_problem &p)
 {
     const double rows = (double)(p.T * p.K) / (double)p.E;
-    return rows <= 20 ? 32 : rows <= 44 ? 64 : rows <= 1024 ? 128 : 256;
+    const int64_t tiles = moe::max_mtiles_bound(p.T * p.K, (int)p.E, 32) *
+                          ((std::max(p.H, p.I) + 31) / 32);
+    return rows <= 20 || tiles <= 1024 ? 32 : rows <= 48 || tiles <= 8192 ? 64 : 128;
 }
 
 MxFwdLayout mx_fwd_layout(const moe_ffn_problem &p, int bits)
@@ -1549,6 +1565,7 @@ int moe_ffn_mxfp4_fwd(const moe_ffn_problem *p, int32_t act_format, const void *
     g.act_srow = L.act.scale_row();
     g.BM = L.BM;
     g.o = at<void>(ws, L.o);
+    g.stream_o = TK * p->H * 2 > ((int64_t)192 << 20); // where the combine reads it past the cache
 
     moe::MxGemmArgs g1 = g;
     const MxWeightLayout up = mx_weight_layout(p->E, p->H, 2 * p->I, 2);

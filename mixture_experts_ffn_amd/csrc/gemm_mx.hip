@@ -13,6 +13,7 @@
 namespace moe {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 // A lane's codes of one block of the token operand.
 template <int BITS> struct MxFrag {
@@ -342,7 +343,6 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxGemmArgs a)
             for (int q = 0; q < 4; ++q) {
                 const int col = c * 32 + 8 * q + 4 * h;
                 if (live && col < a.N) {
-                    typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
                     const bf16x4 out = {(bf16)sum[4 * q], (bf16)sum[4 * q + 1],
                                         (bf16)sum[4 * q + 2], (bf16)sum[4 * q + 3]};
                     *reinterpret_cast<bf16x4 *>(orow + col) = out;
@@ -355,17 +355,17 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxGemmArgs a)
     }
 }
 
-// Tile kernel.  A tile is 32 TF WR token rows of one expert times eight column
-// tiles; a wave has 32 TF rows of two of them: GEMM1 a gate tile and the up tile of the same columns (so
+// Tile kernel.  A tile is 32 TF token rows of one expert times eight column
+// tiles, two a wave: GEMM1 a gate tile and the up tile of the same columns (so
 // the epilogue stays in the wave), GEMM2 two neighbours.  The weights go from
 // memory straight into registers, since the waves share none; the token rows,
 // which all four waves read, are copied into a ring of LDS stages of two
 // k-steps, 64 bytes of codes a row, swizzled like the bf16 kernels' rows.
-template <int BITS, bool G1, int TF, int WR>
-__global__ __launch_bounds__(256 * WR, TF == 4 ? 2 : 3) void mx_tile_kernel(MxGemmArgs a)
+template <int BITS, bool G1, int TF>
+__global__ __launch_bounds__(256, TF == 4 ? 2 : 3) void mx_tile_kernel(MxGemmArgs a)
 {
     using namespace tile;
-    constexpr int ROWS = WR * TF * 32;
+    constexpr int ROWS = TF * 32;
     constexpr int CODES = ROWS * 64, TAILS = BITS == 6 ? ROWS * 32 : 0, SCALES = ROWS * 16;
     constexpr int STAGE = CODES + TAILS, RING = 4;
     constexpr int NC = TF / 2;                       // code copies of a wave and stage
@@ -374,7 +374,6 @@ __global__ __launch_bounds__(256 * WR, TF == 4 ? 2 : 3) void mx_tile_kernel(MxGe
     __shared__ __attribute__((aligned(1024))) unsigned char smem[RING * STAGE + 2 * SCALES];
     unsigned char *const sscale = smem + RING * STAGE;
     const int wave = uni(threadIdx.x >> 6);
-    const int wr = wave >> 2, wn = wave & 3; // wave row, wave column
     constexpr int PER = G1 ? 4 : 8; // column tiles of a panel
     const int ncg = (a.NT + PER - 1) / PER;
     const int KP = a.KS >> 1; // stages
@@ -387,7 +386,6 @@ __global__ __launch_bounds__(256 * WR, TF == 4 ? 2 : 3) void mx_tile_kernel(MxGe
         int lane = threadIdx.x & 63;
         asm volatile("" : "+v"(lane));
         const int h = lane >> 5, fr = lane & 31;
-        const int row0 = wr * (TF * 32); // this wave's rows of the tile
         // expert-major; inside an expert groups of up to 8 M-tiles, column
         // groups outer and M-tiles inner, so that tiles in flight share weights
         const int e = ldc(a.mtile_expert, (int)(t / ncg));
@@ -430,7 +428,7 @@ __global__ __launch_bounds__(256 * WR, TF == 4 ? 2 : 3) void mx_tile_kernel(MxGe
         int tl[2]; // the wave's column tiles
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            tl[j] = uni(min(cg * PER + (G1 ? wn : 2 * wn + j), a.NT - 1) + (G1 ? j * a.NT : 0));
+            tl[j] = uni(min(cg * PER + (G1 ? wave : 2 * wave + j), a.NT - 1) + (G1 ? j * a.NT : 0));
         const uint32_t wl = lane * 16, sl = lane * 4;
         // copies of stage p (past the end: of the last one, into a stage that is not read again)
         auto copy = [&](int p) {
@@ -486,13 +484,13 @@ __global__ __launch_bounds__(256 * WR, TF == 4 ? 2 : 3) void mx_tile_kernel(MxGe
             int as[TF];
 #pragma unroll
             for (int f = 0; f < TF; ++f)
-                as[f] = *reinterpret_cast<const int *>(sc + (row0 + f * 32 + fr) * 16);
+                as[f] = *reinterpret_cast<const int *>(sc + (f * 32 + fr) * 16);
             auto step = [&](auto H) {
                 constexpr int s = decltype(H)::value;
                 constexpr int sel = 2 * decltype(ODD)::value + s;
 #pragma unroll
                 for (int f = 0; f < TF; ++f) {
-                    const int r = row0 + f * 32 + fr;
+                    const int r = f * 32 + fr;
                     MxFrag<BITS> av;
                     av.c = *reinterpret_cast<const u32x4 *>(st + r * 64 + aswz<4>(r, 2 * s + h) * 16);
                     if constexpr (BITS == 6)
@@ -542,10 +540,10 @@ __global__ __launch_bounds__(256 * WR, TF == 4 ? 2 : 3) void mx_tile_kernel(MxGe
         lds_barrier();
         // the last barrier: every wave is past its reads, so the next tile may copy
         if constexpr (G1) {
-            const int c = cg * 4 + wn;
+            const int c = cg * 4 + wave;
 #pragma unroll
             for (int f = 0; f < TF; ++f) {
-                const int r = row0 + f * 32 + fr;
+                const int r = f * 32 + fr;
                 const bool live = r < nr && c < a.NT;
                 const ActRow ar = act_row<BITS>(a, r0 + min(r, nr - 1));
                 store_act<BITS>(acc[0][f], acc[1][f], ar, c, live);
@@ -553,37 +551,55 @@ __global__ __launch_bounds__(256 * WR, TF == 4 ? 2 : 3) void mx_tile_kernel(MxGe
                     store_empty<BITS>(ar, c + 1, 2 * a.act_KS);
             }
         } else {
+            // The 64 columns of a wave are turned in LDS, 32 rows at a time, so
+            // that a store instruction writes eight rows of 128 bytes; straight
+            // from the registers it would touch 32 rows in pieces of 16 bytes
+            // (65536 x 2048 x 7168, MXFP4: 810 us, this way 697, and 650 with the
+            // stores that pass the cache).  Of four row fragments the turn lies
+            // in the ring's last two stages, which the next tile's copies reach
+            // after a barrier; of two it takes the whole ring.
+            unsigned char *const turn = smem + (TF == 4 ? 2 * STAGE : 0) + wave * 4096;
+            const int part = lane & 7, col = (cg * 8 + 2 * wave) * 32 + part * 8;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int col = (cg * 8 + 2 * wn + j) * 32 + 16 * h;
+            for (int f = 0; f < TF; ++f) {
 #pragma unroll
-                for (int f = 0; f < TF; ++f) {
-                    const int r = row0 + f * 32 + fr;
-                    float v[16];
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        v[i] = acc[j][f][i];
-                    gather_columns(v);
-                    bf16x8 o[2];
+                    for (int q = 0; q < 4; ++q) {
+                        bf16x4 o;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        o[i / 8][i % 8] = (bf16)v[i];
-                    bf16 *dst = static_cast<bf16 *>(a.o) + (int64_t)(r0 + r) * a.N + col;
+                        for (int i = 0; i < 4; ++i)
+                            o[i] = (bf16)acc[j][f][4 * q + i];
+                        *reinterpret_cast<bf16x4 *>(turn + fr * 128 +
+                                                    aswz<8>(fr, j * 4 + q) * 16 + h * 8) = o;
+                    }
+                asm volatile("" ::: "memory"); // a wave's LDS operations complete in order
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) // N is a multiple of 8
-                        if (r < nr && col + 8 * i < a.N)
-                            *reinterpret_cast<bf16x8 *>(dst + 8 * i) = o[i];
+                for (int i = 0; i < 4; ++i) {
+                    const int rl = i * 8 + (lane >> 3), r = f * 32 + rl;
+                    const u32x4 v =
+                        *reinterpret_cast<const u32x4 *>(turn + rl * 128 + aswz<8>(rl, part) * 16);
+                    if (r < nr && col < a.N) { // N is a multiple of 8
+                        u32x4 *dst = reinterpret_cast<u32x4 *>(static_cast<bf16 *>(a.o) +
+                                                               (int64_t)(r0 + r) * a.N + col);
+                        if (a.stream_o)
+                            __builtin_nontemporal_store(v, dst);
+                        else
+                            *dst = v;
+                    }
                 }
+                asm volatile("" ::: "memory");
             }
+            __builtin_amdgcn_s_waitcnt(0xC07F); // LDS only: writes of rows past nr had no reader
+            if (TF == 2)
+                lds_barrier();
         }
     }
 }
 
 template <int BITS, bool G1> static auto tile_kernel(int BM)
 {
-    return BM == 64    ? mx_tile_kernel<BITS, G1, 2, 1>
-           : BM == 128 ? mx_tile_kernel<BITS, G1, 4, 1>
-                       : mx_tile_kernel<BITS, G1, 4, 2>;
+    return BM == 64 ? mx_tile_kernel<BITS, G1, 2> : mx_tile_kernel<BITS, G1, 4>;
 }
 
 hipError_t launch_mx_gemm(bool g1, int bits, const MxGemmArgs &a, int num_cus, hipStream_t s)
@@ -591,7 +607,7 @@ hipError_t launch_mx_gemm(bool g1, int bits, const MxGemmArgs &a, int num_cus, h
     const bool stream = a.BM == 32;
     const int per = stream ? (g1 ? 2 : 4) : (g1 ? 4 : 8);
     const int64_t most = (int64_t)a.max_mtiles * ((a.NT + per - 1) / per);
-    int64_t grid = (int64_t)num_cus * (a.BM == 256 ? 1 : a.BM == 64 ? 3 : 2);
+    int64_t grid = (int64_t)num_cus * (a.BM == 64 ? 3 : 2);
     if (most < grid)
         grid = most;
     grid = (grid + 7) / 8 * 8; // a whole number of workgroups for each XCD
@@ -599,7 +615,7 @@ hipError_t launch_mx_gemm(bool g1, int bits, const MxGemmArgs &a, int num_cus, h
                           : (bits == 4 ? mx_stream_kernel<4, false> : mx_stream_kernel<6, false>))
              : g1   ? (bits == 4 ? tile_kernel<4, true>(a.BM) : tile_kernel<6, true>(a.BM))
                     : (bits == 4 ? tile_kernel<4, false>(a.BM) : tile_kernel<6, false>(a.BM));
-    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(a.BM == 256 ? 512 : 256), 0, s, a);
+    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 

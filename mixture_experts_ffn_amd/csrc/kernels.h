@@ -225,6 +225,7 @@ struct MxGemmArgs {
     const uint8_t *acodes, *atails, *ascales; // GEMM1: token rows; GEMM2: act rows (permuted)
     uint8_t *act_codes, *act_tails, *act_scales; // GEMM1's output, permuted rows
     void *o;                         // GEMM2's output [TK, N] bf16
+    bool stream_o;                   // o does not stay in the last-level cache
     const int32_t *sorted_slot;      // permuted row -> slot
     const int32_t *offsets;          // [E + 1]
     const int32_t *mtile_off;        // [E + 1]
