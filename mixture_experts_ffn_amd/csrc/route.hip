@@ -387,7 +387,8 @@ __global__ __launch_bounds__(64) void route_scatter_kernel(
 // RIDE = 4 or 6: blocks from `nblk` on quantise token rows to that many bits
 // instead.  Routing leaves nearly all of the chip idle and the rows need nothing
 // of it, so the two take the time of the longer one and a launch less (one token
-// of 7168: QBOTH us, 128: ..).
+// of 7168: 5.6 us against 5.4 + 2.0, 128 tokens: 6.4 against 7.0 + 4.7, 4096 of
+// 2048: 13 against 12 + 6.5).
 enum { ROUTE_ONE = 0, ROUTE_SELF = 1, ROUTE_HIST = 2 };
 constexpr int64_t kSelfCountSlots = 32768;
 

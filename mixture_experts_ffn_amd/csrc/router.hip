@@ -550,7 +550,7 @@ __device__ inline void store_slots(const RouterArgs &a, int64_t t, int k, const 
 //
 // Four rows share a wave, and with them what a round of the selection costs
 // whatever the row's length: with 64 lanes a row, 32768 rows of 256 experts in
-// 8 groups take 61 us, here 22.  A key is a double: an fp32 key, exactly, with
+// 8 groups take 50 us, here 23 (their bytes need 7).  A key is a double: an fp32 key, exactly, with
 // the expert's number in the 29 bits below it, so that one maximum finds the
 // largest key, breaks ties towards the lower id and names the expert.
 constexpr uint32_t kClosedHi = 0xD2B00000u; // -2^300: closed or taken
@@ -744,26 +744,30 @@ __global__ __launch_bounds__(256) void router_rows_kernel(RouterArgs a)
                 key[i].hi = keep ? key[i].hi : kClosedHi;
         }
     }
-    int my_id = -1;
-    float last = INFINITY;
-    const int rounds = sums ? a.K + 1 : a.K; // with sums, also the first one left out
-    for (int k = 0; k < rounds; ++k) {
-        const Bits64 m(row_max_d(largest_of<R>(key)));
-        const bool open = m.hi != kClosedHi;
-        if (sums) {
-            const float v = (float)Bits64(m.lo & 0xE0000000u, m.hi).value();
-            ok = ok && (!open || !(last - v <= margin));
-            last = v;
-            if (k == a.K)
-                break;
-        }
-        const uint32_t n = m.lo & 1023u;
-        if (sub == k)
-            my_id = open ? (int32_t)m.hi < 0 ? (int)n : 1023 - (int)n : -1;
+    // lane k keeps slot k's key
+    Bits64 kept(0u, kClosedHi), m;
+    for (int k = 0; k < a.K; ++k) {
+        m = Bits64(row_max_d(largest_of<R>(key)));
+        kept.lo = sub == k ? m.lo : kept.lo;
+        kept.hi = sub == k ? m.hi : kept.hi;
 #pragma unroll
         for (int i = 0; i < R; ++i)
             key[i].hi = key[i].lo == m.lo ? kClosedHi : key[i].hi; // one expert's (256 at most)
     }
+    if (sums) {
+        // each slot against the next, the last against the first one left out
+        m = Bits64(row_max_d(largest_of<R>(key)));
+        Bits64 below(dpp<0x12F>(kept.lo), dpp<0x12F>(kept.hi)); // lane + 1's
+        if (sub == a.K - 1)
+            below = m;
+        const auto number = [](const Bits64 &k) {
+            return (float)Bits64(k.lo & 0xE0000000u, k.hi).value();
+        };
+        const bool near = !(number(kept) - number(below) > margin);
+        ok = ok && !row_any(sub < a.K && below.hi != kClosedHi && near, lane);
+    }
+    const int n = (int)(kept.lo & 1023u);
+    const int my_id = kept.hi == kClosedHi ? -1 : (int32_t)kept.hi < 0 ? n : 1023 - n;
     Slot mine = {my_id, my_id >= 0 ? load_logit(a, t, my_id) : -INFINITY};
     const uint64_t again = KIND == BY_LOGIT ? 0 : __ballot(!ok && here);
     if (again) {
@@ -982,7 +986,8 @@ __device__ inline void join_slots(int K, int id, float d, int sub, float *sum, b
 // Sixteen lanes a row, up to 256 experts and 16 slots: the slots' parts reach
 // their experts' lanes through LDS, and the gradients leave through it, so
 // that a store covers consecutive experts (a lane's own are R apart).  With 64
-// lanes a row, 32768 rows of 256 experts take 18 us and of 64 experts 12.
+// lanes a row, 32768 rows of 256 experts take 18 us and of 64 experts 12, here
+// 9 and 5.
 template <int R>
 __global__ __launch_bounds__(256) void router_bwd_rows_kernel(RouterArgs a)
 {
