@@ -1423,6 +1423,11 @@ int validate_mx_fwd(const moe_ffn_problem *p, int32_t act_format, uint32_t flags
         return fail(MOE_FFN_ERR_SHAPE, "the MXFP4 forward takes no shared expert (Is must be 0)");
     if (p->T * moe::MxDims(p->H, p->I).code_row() >= (int64_t(1) << 32))
         return fail(MOE_FFN_ERR_SHAPE, "T*H must be < 2^33 (4 GiB of quantised tokens)");
+    // the kernels address an expert's codes, 32 columns and 128 values at least,
+    // by 32 bits
+    for (const moe::MxDims &d : {moe::MxDims(p->H, 2 * p->I), moe::MxDims(p->I, p->H)})
+        if ((int64_t)(d.NT + 1) * d.KS * 1024 >= (int64_t(1) << 32))
+            return fail(MOE_FFN_ERR_SHAPE, "an expert's packed weights must be below 4 GiB");
     if (flags & ~(MOE_FFN_CHECK_IDS | MOE_FFN_CHECK_STATUS))
         return fail(MOE_FFN_ERR_SHAPE, "flags: only CHECK_IDS and CHECK_STATUS apply (got 0x%x)",
                     flags);
