@@ -366,8 +366,14 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxGemmArgs a)
 // alone, on random codes in registers, reaches 6.3: the matrix cores are busy
 // half of the time, at 1.8 GHz, to which the power limit takes the clock (codes
 // of zero: 0.89 ms).  GEMM2 writes 0.94 GB of o besides: 0.66 ms.
+//
+// Workgroups of a CU: three with 64 rows and MXFP4, else two; held to the 168
+// registers of three, the MXFP6 kernels spill (128 x 7168 x 2048, 32 experts, top
+// 8: 108 + 56 us against 97 + 51).
+constexpr int tile_groups(int bits, int rows) { return rows == 64 && bits == 4 ? 3 : 2; }
+
 template <int BITS, bool G1, int TF>
-__global__ __launch_bounds__(256, TF == 4 ? 2 : 3) void mx_tile_kernel(MxGemmArgs a)
+__global__ __launch_bounds__(256, tile_groups(BITS, 32 * TF)) void mx_tile_kernel(MxGemmArgs a)
 {
     using namespace tile;
     constexpr int ROWS = TF * 32;
@@ -627,7 +633,7 @@ hipError_t launch_mx_gemm(bool g1, int bits, const MxGemmArgs &a, int num_cus, h
     const int64_t most = (int64_t)a.max_mtiles * ((a.NT + per - 1) / per);
     if (most >= ((int64_t)1 << 31))
         return hipErrorInvalidValue;
-    int64_t grid = (int64_t)num_cus * (a.BM == 64 ? 3 : 2);
+    int64_t grid = (int64_t)num_cus * tile_groups(bits, a.BM);
     if (most < grid)
         grid = most;
     grid = (grid + 7) / 8 * 8; // a whole number of workgroups for each XCD
