@@ -27,6 +27,7 @@ import re
 import threading
 
 import torch
+from torch.autograd.function import once_differentiable
 
 __all__ = [
     "MoEFFNError",
@@ -673,6 +674,7 @@ class MoERouterFunction(torch.autograd.Function):
         return weights, ids
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_weights, _):
         logits, ids = ctx.saved_tensors
         d_logits = moe_ffn_router_bwd(d_weights.contiguous(), logits, ids, **ctx.form)
@@ -693,6 +695,7 @@ class MXFP4Weight:
 
     def __init__(self, data, E, Kd, N, panels, dtype):
         self.data, self.E, self.Kd, self.N, self.panels, self.dtype = data, E, Kd, N, panels, dtype
+        self.nbytes = _mxfp4_weight_size(self._stack())
 
     def _stack(self):
         return MXFP4Stack(self.E, self.Kd, self.N, self.panels,
@@ -768,6 +771,8 @@ def moe_ffn_mxfp4_fwd(x, topk_ids, topk_weights, up: MXFP4Weight, down: MXFP4Wei
     if (up.E, up.Kd, up.N, up.panels) != (E, H, 2 * I, 2) or (down.N, down.panels) != (H, 1):
         raise MoEFFNError(2, "expected up packed from [E, H, 2I] with 2 panels and down from "
                              "[E, I, H] with 1")
+    if up.data.nbytes < up.nbytes or down.data.nbytes < down.nbytes:
+        raise MoEFFNError(5, "packed weights shorter than their sizes need")
     prob = Problem(T, H, I, E, topk_ids.shape[1], _dtype_code(x), _ids_code(topk_ids))
     flags |= CHECK_IDS if check_ids else 0
     dev = x.device

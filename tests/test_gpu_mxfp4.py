@@ -303,6 +303,19 @@ def test_ffn_refusals(gpu_lib):
     assert m.moe_ffn_mxfp4_fwd(x[:0], ids[:0], gates[:0], pu, pd).shape == (0, 64)
 
 
+def test_short_packed_weights_are_refused(gpu_lib):
+    m = gpu_lib
+    x, ids, gates, up, down = make(8, 64, 32, 4, 2)
+    x, ids, gates = x.cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(gates).cuda()
+    pu, pd = m.moe_ffn_mxfp4_quantize(up.cuda(), panels=2), m.moe_ffn_mxfp4_quantize(down.cuda())
+    short = lambda p: m.MXFP4Weight(p.data[:-16], p.E, p.Kd, p.N, p.panels, p.dtype)
+    for u, d in ((short(pu), pd), (pu, short(pd))):
+        with pytest.raises(m.MoEFFNError):
+            m.moe_ffn_mxfp4_fwd(x, ids, gates, u, d)
+    with pytest.raises(m.MoEFFNError):
+        m.moe_ffn_mxfp4_dequantize(short(pd))
+
+
 def test_router_into_quantised_layer(gpu_lib):
     """A serving step: logits, router, quantised experts; a padded token and a closed expert."""
     say("[mxfp4] router into the layer")

@@ -268,6 +268,14 @@ def test_autograd_with_the_layer(gpu_lib, form):
     assert (err <= (64 + 2 * spread(l.numpy())) * U * mag).all()
 
 
+def test_second_derivative_is_refused(gpu_lib):
+    l = torch.randn(6, 16, device="cuda", requires_grad=True)
+    w, _ = gpu_lib.moe_ffn_router(l, 2)
+    g, = torch.autograd.grad((w * w).sum(), l, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
+
+
 def test_graph_replays_and_other_streams(gpu_lib):
     say("[router] graph and streams")
     l = torch.randn(300, 64, device="cuda")
