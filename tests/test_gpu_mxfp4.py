@@ -168,6 +168,29 @@ def test_ffn_sizes(gpu_lib, shape, act):
     check(gpu_lib, make(*shape), act)
 
 
+# more 32-row tiles than the waves that split a contraction are used for: 64-row tiles, and from
+# 8192 of them on, and more than 48 rows an expert, 128-row tiles
+TALL = [(1050, 520, 72, 2, 2), (900, 72, 1032, 2, 2), (1111, 1000, 200, 5, 2), (2049, 1032, 40, 1, 1),
+        (1100, 2056, 1032, 1, 1), (1500, 264, 200, 64, 2), (130, 1032, 72, 16, 8),
+        (4100, 2056, 40, 2, 1), (4033, 40, 2056, 2, 1), (3000, 1000, 264, 12, 4),
+        (820, 2056, 136, 5, 5), (4097, 2056, 1032, 1, 1), (4200, 2120, 8, 3, 1)]
+
+
+@pytest.mark.parametrize("act", ["mxfp4", "mxfp6"])
+@pytest.mark.parametrize("shape", TALL, ids=str)
+def test_ffn_sizes_of_tall_tiles(gpu_lib, shape, act):
+    say(f"[mxfp4] ffn {shape} {act}")
+    check(gpu_lib, make(*shape, seed=10), act)
+
+
+@pytest.mark.parametrize("act", ["mxfp4", "mxfp6"])
+@pytest.mark.parametrize("routing", ["replace", "one"])
+@pytest.mark.parametrize("shape", [(1100, 1032, 136, 9, 4), (1400, 1544, 136, 9, 4)], ids=str)
+def test_ffn_routings_of_tall_tiles(gpu_lib, shape, routing, act):
+    say(f"[mxfp4] ffn {shape} routing={routing} {act}")
+    check(gpu_lib, make(*shape, seed=11, routing=routing, empty=(0, 3, 8)), act)
+
+
 @pytest.mark.parametrize("act", ["mxfp4", "mxfp6"])
 @pytest.mark.parametrize("shape", [(4100, 40, 32, 5, 3), (8200, 72, 24, 9, 5), (650, 64, 32, 1000, 2),
                                    (9, 64, 32, 1024, 5)], ids=str)
@@ -223,6 +246,12 @@ def test_nan_and_infinity_stay_in_their_token(gpu_lib, shape, act):
     bad[[3, 17, 18]] = True
     assert y[bad].isnan().all()
     assert torch.equal(y[~bad], clean[~bad])
+
+
+@pytest.mark.parametrize("act", ["mxfp4", "mxfp6"])
+@pytest.mark.parametrize("shape", [(1100, 1032, 72, 2, 1), (4200, 2056, 72, 2, 1)], ids=str)
+def test_nan_and_infinity_in_tall_tiles(gpu_lib, shape, act):
+    test_nan_and_infinity_stay_in_their_token(gpu_lib, shape, act)
 
 
 @pytest.mark.parametrize("act", ["mxfp4", "mxfp6"])
