@@ -695,7 +695,14 @@ class MXFP4Weight:
 
     def __init__(self, data, E, Kd, N, panels, dtype):
         self.data, self.E, self.Kd, self.N, self.panels, self.dtype = data, E, Kd, N, panels, dtype
-        self.nbytes = _mxfp4_weight_size(self._stack())
+        self._nbytes = None
+
+    @property
+    def nbytes(self) -> int:
+        """Bytes that ``data`` must hold."""
+        if self._nbytes is None:
+            self._nbytes = _mxfp4_weight_size(self._stack())
+        return self._nbytes
 
     def _stack(self):
         return MXFP4Stack(self.E, self.Kd, self.N, self.panels,
