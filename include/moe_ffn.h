@@ -468,8 +468,9 @@ int moe_ffn_mxfp4_workspace_size(const moe_ffn_problem *p, int32_t act_format, u
  * moe_ffn_fwd.  A NaN or infinity in a token's row makes that token's
  * output NaN and no other's.  dtype must be BF16 and Is 0; the flags
  * MOE_FFN_CHECK_IDS and MOE_FFN_CHECK_STATUS apply, others are rejected with
- * MOE_FFN_ERR_SHAPE, and so are calls whose quantised tokens (T · H / 2 bytes, H
- * rounded up to 128) or one expert's packed weights reach 4 GiB. */
+ * MOE_FFN_ERR_SHAPE, and so are calls of 2^24 tokens or more, and those whose
+ * quantised tokens (T · H / 2 bytes, H rounded up to 128) or one expert's packed
+ * weights reach 4 GiB. */
 int moe_ffn_mxfp4_fwd(const moe_ffn_problem *p, int32_t act_format, const void *x,
                       const void *topk_ids, const float *topk_weights, const void *up_packed,
                       const void *down_packed, void *y, void *ws, size_t ws_bytes, uint32_t flags,

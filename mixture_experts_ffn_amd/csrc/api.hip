@@ -1375,9 +1375,11 @@ int mx_tile_rows(const moe_ffn_problem &p)
     return rows <= 20 || tiles <= 1024 ? 32 : rows <= 48 || tiles <= 8192 ? 64 : 128;
 }
 
-MxFwdLayout mx_fwd_layout(const moe_ffn_problem &p, int bits)
+void mx_fwd_layout(const moe_ffn_problem &p, int bits, MxFwdLayout &L)
 {
-    MxFwdLayout L{{}, mx_tile_rows(p), 0, moe::MxDims(p.H, p.I), moe::MxDims(p.I, p.H)};
+    L.BM = mx_tile_rows(p);
+    L.x = moe::MxDims(p.H, p.I);
+    L.act = moe::MxDims(p.I, p.H);
     const int64_t TK = p.T * p.K;
     const int E = (int)p.E;
     L.rp = moe::make_route_plan(TK, E);
@@ -1406,7 +1408,6 @@ MxFwdLayout mx_fwd_layout(const moe_ffn_problem &p, int bits)
     L.act_scales = take((size_t)TK * L.act.scale_row());
     L.o = take(2 * (size_t)TK * (size_t)p.H);
     L.total = off;
-    return L;
 }
 
 int validate_mx_fwd(const moe_ffn_problem *p, int32_t act_format, uint32_t flags)
@@ -1423,6 +1424,8 @@ int validate_mx_fwd(const moe_ffn_problem *p, int32_t act_format, uint32_t flags
         return fail(MOE_FFN_ERR_SHAPE, "the MXFP4 forward takes no shared expert (Is must be 0)");
     if (p->T * moe::MxDims(p->H, p->I).code_row() >= (int64_t(1) << 32))
         return fail(MOE_FFN_ERR_SHAPE, "T*H must be < 2^33 (4 GiB of quantised tokens)");
+    if (p->T >= (int64_t(1) << 24)) // a workgroup of 256 threads a token in the combine
+        return fail(MOE_FFN_ERR_SHAPE, "T must be < 2^24 (got %lld)", (long long)p->T);
     // the kernels address an expert's codes, 32 columns and 128 values at least,
     // by 32 bits
     for (const moe::MxDims &d : {moe::MxDims(p->H, 2 * p->I), moe::MxDims(p->I, p->H)})
@@ -1498,7 +1501,9 @@ int moe_ffn_mxfp4_workspace_size(const moe_ffn_problem *p, int32_t act_format, u
         return rc;
     if (!ws_bytes)
         return fail(MOE_FFN_ERR_NULL, "ws_bytes is NULL");
-    *ws_bytes = mx_fwd_layout(*p, act_format == MOE_FFN_MXFP4 ? 4 : 6).total;
+    MxFwdLayout L;
+    mx_fwd_layout(*p, act_format == MOE_FFN_MXFP4 ? 4 : 6, L);
+    *ws_bytes = L.total;
     return MOE_FFN_OK;
 }
 
@@ -1514,7 +1519,8 @@ int moe_ffn_mxfp4_fwd(const moe_ffn_problem *p, int32_t act_format, const void *
     if (p->T == 0)
         return MOE_FFN_OK;
     const int bits = act_format == MOE_FFN_MXFP4 ? 4 : 6;
-    const MxFwdLayout L = mx_fwd_layout(*p, bits);
+    MxFwdLayout L;
+    mx_fwd_layout(*p, bits, L);
     if ((rc = check_ptr(x, "x")) ||
         (rc = check_ptr(topk_ids, "topk_ids", p->ids_dtype == MOE_FFN_I64 ? 8 : 4)) ||
         (rc = check_ptr(topk_weights, "topk_weights", 4)) ||

@@ -52,6 +52,7 @@ constexpr int kMxNan = 255;  // E8M0 code of NaN
 
 struct MxDims {
     int NT, KS, KC;
+    MxDims() = default;
     __host__ __device__ MxDims(int64_t Kd, int64_t panel_cols)
         : NT((int)((panel_cols + 31) / 32)), KS((int)((Kd + 127) / 128) * 2), KC((KS + 3) / 4)
     {

@@ -1111,18 +1111,8 @@ template <int KIND> static hipError_t launch_fwd(const RouterArgs &a, hipStream_
     return hipGetLastError();
 }
 
-hipError_t launch_router_fwd(const RouterArgs &in, hipStream_t s)
+static hipError_t launch_bwd(const RouterArgs &a, hipStream_t s)
 {
-    const RouterArgs a = prepared(in);
-    const bool grouped = a.topk_groups < a.groups;
-    if (a.bias || (grouped && a.group_top == 2))
-        return a.sigmoid ? launch_fwd<BY_SIGMOID>(a, s) : launch_fwd<BY_SOFTMAX>(a, s);
-    return grouped ? launch_fwd<BY_LOGIT_GROUPED>(a, s) : launch_fwd<BY_LOGIT>(a, s);
-}
-
-hipError_t launch_router_bwd(const RouterArgs &in, hipStream_t s)
-{
-    const RouterArgs a = prepared(in);
     if (a.E <= 256 && a.K <= 16) {
         auto rows = a.E <= 16    ? router_bwd_rows_kernel<1>
                     : a.E <= 32  ? router_bwd_rows_kernel<2>
@@ -1139,6 +1129,46 @@ hipError_t launch_router_bwd(const RouterArgs &in, hipStream_t s)
                           : router_bwd_kernel<16>;
     hipLaunchKernelGGL(k, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, s, a);
     return hipGetLastError();
+}
+
+// A launch has fewer than 2^32 threads, up to 64 a row: longer batches take
+// several, of 2^25 rows.
+template <typename F> static hipError_t in_parts(const RouterArgs &in, F launch)
+{
+    constexpr int64_t ROWS = (int64_t)1 << 25;
+    const RouterArgs a = prepared(in);
+    const int64_t es = a.bf16 ? 2 : 4, is = a.ids64 ? 8 : 4;
+    for (int64_t t0 = 0; t0 < a.T; t0 += ROWS) {
+        RouterArgs p = a;
+        p.T = a.T - t0 < ROWS ? a.T - t0 : ROWS;
+        p.logits = static_cast<const char *>(a.logits) + t0 * a.stride * es;
+        p.ids = static_cast<char *>(a.ids) + t0 * a.K * is;
+        if (a.d_logits) {
+            p.d_weights = a.d_weights + t0 * a.K;
+            p.d_logits = static_cast<char *>(a.d_logits) + t0 * a.E * es;
+        } else {
+            p.weights = a.weights + t0 * a.K;
+        }
+        const hipError_t err = launch(p);
+        if (err != hipSuccess)
+            return err;
+    }
+    return hipSuccess;
+}
+
+hipError_t launch_router_fwd(const RouterArgs &in, hipStream_t s)
+{
+    return in_parts(in, [&](const RouterArgs &a) {
+        const bool grouped = a.topk_groups < a.groups;
+        if (a.bias || (grouped && a.group_top == 2))
+            return a.sigmoid ? launch_fwd<BY_SIGMOID>(a, s) : launch_fwd<BY_SOFTMAX>(a, s);
+        return grouped ? launch_fwd<BY_LOGIT_GROUPED>(a, s) : launch_fwd<BY_LOGIT>(a, s);
+    });
+}
+
+hipError_t launch_router_bwd(const RouterArgs &in, hipStream_t s)
+{
+    return in_parts(in, [&](const RouterArgs &a) { return launch_bwd(a, s); });
 }
 
 } // namespace moe

@@ -325,3 +325,21 @@ def test_long_batch_with_rows_past_32_bit_offsets(gpu_lib):
     d2 = gpu_lib.moe_ffn_router_bwd(dw[-700:].contiguous(), tail, ids2, renormalize=False)
     assert torch.equal(ids[-700:], ids2) and torch.equal(w[-700:], w2)
     assert torch.equal(d[-700:], d2)
+
+
+@pytest.mark.parametrize("T,E,K", [((1 << 28) + 37, 2, 1), ((1 << 26) + 21, 17, 17)], ids=str)
+def test_batches_of_more_rows_than_a_launch_takes(gpu_lib, T, E, K):
+    """Every row as in a small batch: the rows repeat a table of 2^16 + 1, so no part looks like another."""
+    say(f"[router] T={T} E={E} K={K}")
+    n = (1 << 16) + 1
+    table = torch.randn(n, E, device="cuda").bfloat16()
+    l = table.repeat(T // n + 1, 1)[:T]
+    dw = torch.randn(n, K, device="cuda").repeat(T // n + 1, 1)[:T]
+    w0, i0 = gpu_lib.moe_ffn_router_fwd(table, K)
+    d0 = gpu_lib.moe_ffn_router_bwd(dw[:n], table, i0, renormalize=False)
+    w, ids = gpu_lib.moe_ffn_router_fwd(l, K)
+    d = gpu_lib.moe_ffn_router_bwd(dw, l, ids, renormalize=False)
+    for got, ref in ((w, w0), (ids, i0), (d, d0)):
+        whole = T // n * n
+        assert (got[:whole].view(T // n, -1) == ref.view(1, -1)).all()
+        assert torch.equal(got[whole:], ref[:T - whole])

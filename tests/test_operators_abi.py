@@ -107,6 +107,7 @@ def prob(**kw):
     (dict(H=12), 4, 0, 2), (dict(K=0), 4, 0, 2), (dict(dtype=m.F32), 4, 0, 3), (dict(), 3, 0, 3),
     (dict(), 6, 0, 3), (dict(Is=128), 4, 0, 2), (dict(), 4, m.PIPELINE, 2), (dict(), 5, m.BULK, 2),
     (dict(), 4, 0x100, 2), (dict(T=1 << 22, H=2048), 4, 0, 2), (dict(T=(1 << 21) + 1, H=4000), 5, 0, 2),
+    (dict(T=1 << 24, H=8), 4, 0, 2),
     (dict(T=1, H=(1 << 27) - 8, I=8), 4, 0, 2), (dict(T=1, H=8, I=(1 << 27) - 8), 4, 0, 2),
 ])
 def test_forward_rejects(lib, bad, act, flags, code):
