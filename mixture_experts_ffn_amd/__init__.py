@@ -603,8 +603,9 @@ def _router(logits, K, ids_dtype, score, renormalize, groups, topk_groups, group
 
 
 def _same_device(t, *others):
+    index = t.get_device()
     for o in others:
-        if o is not None and o.device != t.device:
+        if o is not None and o.get_device() != index:
             raise MoEFFNError(1, f"tensors on {t.device} and {o.device}: one device is needed")
 
 
