@@ -391,8 +391,12 @@ __global__ __launch_bounds__(256, tile_groups(BITS, 32 * TF)) void mx_tile_kerne
     const int total = uni(ldc(a.mtile_off, a.E)) * ncg; // below 2^31 (checked at launch)
     const int xcd = blockIdx.x & 7;
     const int t1 = (int)((int64_t)total * (xcd + 1) / 8), dt = gridDim.x >> 3;
-    // expert-major; inside an expert groups of up to 8 M-tiles, column groups
-    // outer and M-tiles inner, so that tiles in flight share weights
+    // expert-major; inside an expert groups of up to GM M-tiles, column groups
+    // outer and M-tiles inner, so that tiles in flight share weights and rows.
+    // GEMM2 with 8: 704 us for 65536 x 2048 x 7168 over 32 experts and 157 for
+    // 32768 x 1536 x 4096 over 16, with 4: 665 and 146 (131072 x 1408 x 2048 over
+    // 8 the other way, 274 and 288); GEMM1 the same within noise
+    constexpr int GM = G1 ? 8 : 4;
     struct Place {
         int e, cg, r0, nr; // expert, column group, first row, rows
     };
@@ -401,19 +405,11 @@ __global__ __launch_bounds__(256, tile_groups(BITS, 32 * TF)) void mx_tile_kerne
         q.e = ldc(a.mtile_expert, uni((int)((unsigned)t / (unsigned)ncg)));
         const int mt0 = ldc(a.mtile_off, q.e), mts = ldc(a.mtile_off, q.e + 1) - mt0;
         const unsigned local = t - mt0 * ncg;
-        const int grp = uni(local / (8u * ncg));
-        const unsigned gm = min(mts - grp * 8, 8);
-        const unsigned rr = local - grp * 8 * ncg;
+        const int grp = uni(local / (unsigned)(GM * ncg));
+        const unsigned gm = min(mts - grp * GM, GM);
+        const unsigned rr = local - grp * GM * ncg;
         q.cg = uni(rr / gm);
-        int mt = grp * 8 + (int)(rr - q.cg * gm);
-        if (gm == 8 && (rr | 63u) < 8u * ncg) {
-            // 64 tiles of 8 x 8, those 32 apart in one column group: an XCD's 32
-            // CUs take workgroups in turn, so the two of a CU read the same
-            // weights (65536 x 2048 x 7168: 704 -> 659 us; GEMM1 the same)
-            const unsigned r = rr & 63u;
-            mt = grp * 8 + (int)((r >> 5) * 4 + (r & 3u));
-            q.cg = uni((rr >> 6) * 8 + ((r & 31u) >> 2));
-        }
+        const int mt = grp * GM + (int)(rr - q.cg * gm);
         q.r0 = ldc(a.offsets, q.e) + mt * ROWS;
         q.nr = min(ROWS, ldc(a.offsets, q.e + 1) - q.r0);
         return q;
