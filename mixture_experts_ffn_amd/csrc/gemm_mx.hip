@@ -1,7 +1,9 @@
 // gemm_mx.hip — grouped GEMMs of the expert FFN on MXFP4 weights.
 //
 // GEMM1: act[p, :] = silu(g) * u, [g u] = x[token(p)] . W1[e], quantised to the
-// activation format in the epilogue; GEMM2: o[p, :] = act[p] . W2[e], bf16.
+// activation format in the epilogue; GEMM2: o[p, :] = act[p] . W2[e], rounded to
+// bf16 as in the bf16 layer: half the bytes that GEMM2 writes and the combine
+// reads (0.36 of 1.84 ms for the skewed workload), for at most 2^-8 of each term.
 // Both run on the scaled matrix instruction of 32 x 32 x 64 (mx.h) with the
 // weights as the first operand (its rows are weight columns) and the token rows
 // as the second: a lane then holds 16 weight columns of one token, so a block

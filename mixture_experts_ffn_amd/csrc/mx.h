@@ -46,8 +46,6 @@
 
 namespace moe {
 
-constexpr int kMxBlock = 32; // values that share a scale
-constexpr int kMxStep = 64;  // k of one matrix instruction
 constexpr int kMxNan = 255;  // E8M0 code of NaN
 
 struct MxDims {
