@@ -249,21 +249,28 @@ __device__ inline Slot select_exact(const RouterArgs &a, int64_t t, int lane, do
             for (int i = 0; i < R; ++i)
                 key[i] /= total;
         }
-        if (a.bias) {
-            float b[R];
-            load_bias<R>(a, lane, b);
-#pragma unroll
-            for (int i = 0; i < R; ++i)
-                key[i] += (double)b[i];
-        }
     } else {
 #pragma unroll
         for (int i = 0; i < R; ++i)
             key[i] = (double)l[i];
     }
+    bool closed[R];
 #pragma unroll
     for (int i = 0; i < R; ++i)
-        key[i] = l[i] == -INFINITY ? -INFINITY : isnan(key[i]) ? -DBL_MAX : key[i];
+        closed[i] = l[i] == -INFINITY;
+    if (a.bias) {
+        float b[R];
+        load_bias<R>(a, lane, b);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            key[i] += (double)b[i];
+            closed[i] |= b[i] == -INFINITY;
+        }
+    }
+    // closed before NaN: a NaN score and a bias of -inf add up to NaN
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        key[i] = closed[i] ? -INFINITY : isnan(key[i]) ? -DBL_MAX : key[i];
     if (grouped) {
 #pragma unroll
         for (int i = 0; i < R; ++i)

@@ -42,7 +42,8 @@ def router(logits, K, bias=None, score="softmax", renormalize=True, groups=1, to
         s = _scores(l, score)
         closed = l == -np.inf
         key = l.copy() if bias is None else s + np.asarray(bias, np.float64)
-        closed |= key == -np.inf
+        if bias is not None:
+            closed |= np.asarray(bias) == -np.inf
         key = np.where(np.isnan(key), -np.finfo(np.float64).max, key)
         key[closed] = -np.inf
         if topk_groups < groups:

@@ -1,0 +1,85 @@
+"""The router on rows with NaN, infinities and switched-off experts, against values worked out by
+hand: which experts are chosen must not depend on what else stands in the row."""
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import say
+from oracle import operators as ops
+
+INF, NAN = float("inf"), float("nan")
+
+
+def oracle(logits, K, **kw):
+    bias = kw.pop("bias", None)
+    with np.errstate(all="ignore"):
+        return ops.router(np.array(logits, np.float32), K,
+                          bias=None if bias is None else np.array(bias, np.float32), **kw)
+
+
+def on_gpu(m, logits, K, bias=None, pad=0, **kw):
+    """The kernels' answer, with ``pad`` closed experts behind the row's own: above 256 experts
+    one wave takes a row, up to there sixteen lanes."""
+    l = torch.tensor(logits, dtype=torch.float32)
+    l = torch.nn.functional.pad(l, (0, pad), value=-INF).cuda()
+    b = None
+    if bias is not None:
+        b = torch.nn.functional.pad(torch.tensor(bias, dtype=torch.float32), (0, pad)).cuda()
+    w, ids = m.moe_ffn_router_fwd(l, K, bias=b, **kw)
+    torch.cuda.synchronize()
+    return w.cpu().numpy(), ids.cpu().numpy()
+
+
+# (score, logits, bias, ids of K = 3, which of the three gates are NaN)
+CLOSED = [
+    # one NaN makes every softmax score NaN: the open experts in their order, the closed one never
+    ("softmax", [NAN, 1, 2, 3], [0, -INF, 0, 0], [0, 2, 3], [1, 1, 1]),
+    ("softmax", [0, INF, 1, 2], [-INF, 0, 0, 0], [1, 2, 3], [1, 1, 1]),
+    ("softmax", [NAN, 1, 2, 3], [-INF, -INF, -INF, 0], [3, -1, -1], [1, 0, 0]),
+    # sigmoid: NaN at 0 is closed, NaN at 2 is open and below every number
+    ("sigmoid", [NAN, 1, NAN, 3], [-INF, 0, 0, 0], [3, 1, 2], [0, 0, 1]),
+    ("sigmoid", [1, NAN, NAN, 3], [0, -INF, -INF, 0], [3, 0, -1], [0, 0, 0]),
+    ("sigmoid", [INF, NAN, 0, -INF], [-INF, 0, 0, 0], [2, 1, -1], [0, 1, 0]),
+]
+
+
+def expect_closed(answer):
+    for score, l, bias, ids, nan in CLOSED:
+        say("[router] closed by the bias", score, l, bias)
+        w, got = answer([l], 3, bias=bias, score=score, renormalize=False)
+        assert got.tolist() == [ids], (score, l, bias)
+        assert np.isnan(w).tolist() == [[bool(n) for n in nan]], (score, l, bias)
+        assert (w[got < 0] == 0).all()
+
+
+def test_oracle_closed_by_the_bias():
+    expect_closed(oracle)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("pad", [0, 12, 252, 253, 600])
+def test_closed_by_the_bias(gpu_lib, pad):
+    expect_closed(lambda l, K, **kw: on_gpu(gpu_lib, l, K, pad=pad, **kw))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(64, 1), (64, 8), (256, 8), (160, 8), (512, 1), (512, 16)])
+def test_random_rows_with_every_kind_of_value(gpu_lib, E, groups, score):
+    """NaN, +inf and -inf strewn over logits and -inf over the bias: ids as the oracle's, and an
+    expert whose bias is -inf in no slot."""
+    say("[router] strewn", E, groups, score)
+    rng = np.random.default_rng([E, groups])
+    T, K = 300, 6
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    for value in (NAN, INF, -INF):
+        l[rng.random((T, E)) < 0.3 * rng.random((T, 1)) ** 3] = value
+    bias = (0.2 * rng.standard_normal(E)).astype(np.float32)
+    bias[rng.random(E) < 0.3] = -INF
+    kw = dict(score=score, groups=groups, topk_groups=max(1, groups // 2))
+    w, ids = on_gpu(gpu_lib, l, K, bias=bias, **kw)
+    rw, rid = oracle(l, K, bias=bias, **kw)
+    np.testing.assert_array_equal(ids, rid)
+    assert not np.isin(np.nonzero(bias == -INF)[0], ids).any()
+    np.testing.assert_array_equal(np.isnan(w), np.isnan(rw))
