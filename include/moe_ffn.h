@@ -388,14 +388,16 @@ int moe_ffn_bwd_w(const moe_ffn_problem *p, const void *dy, const void *x, const
  * `groups` > 1 with topk_groups < groups first keeps the topk_groups groups
  * (of E / groups consecutive experts) with the largest value, the value being
  * the group's largest key (group_top 1) or the sum of its two largest
- * (group_top 2), ties to the lower group.  Scores that are added up before
- * they are compared are formed and compared in 64 bits.
+ * (group_top 2), ties to the lower group; a group with fewer than group_top
+ * open experts has the lowest value.  Scores that are added up before they are
+ * compared are formed and compared in 64 bits.
  *
  * An expert whose logit or bias is -inf is closed to that token.  A slot left
  * without an open expert (a padded token's row of -inf, say) gets id -1 and
  * gate 0: moe_ffn_fwd drops such a slot (and records MOE_FFN_DEV_BAD_ID).  A
- * NaN key is below every number; under softmax a NaN or +inf logit makes all
- * gates of its row NaN.
+ * NaN key is below every number, and the sum of two keys with a NaN among them
+ * below every other sum; under softmax a NaN or +inf logit makes all gates of
+ * its row NaN.
  *
  * Limits: those of moe_ffn_problem for T, K and E; K <= E and at most the
  * topk_groups · E / groups experts of the kept groups; groups <= 64 divides E;

@@ -7,7 +7,9 @@
 //   ids    = the K open experts of largest key, ties to the lower id
 //   w_k    = scale * s_k, or scale * s_k / sum of the selected s
 // An expert whose logit (or bias) is -inf is closed; slots left without an
-// open expert get id -1 and gate 0.  A NaN key is below every number.
+// open expert get id -1 and gate 0.  A NaN key is below every number, a sum of
+// two keys with a NaN below every sum without; a group with fewer open experts
+// than its value adds up has the lowest value.
 //
 // Gradients (u_k = s_k / sum of the selected s, g_k = scale * d w_k):
 //   softmax, renormalised  dl_k = u_k (g_k - sum_i g_i u_i)
@@ -15,8 +17,6 @@
 //   sigmoid, renormalised  dl_k = u_k (1 - s_k) (g_k - sum_i g_i u_i)
 //   sigmoid                dl_k = g_k s_k (1 - s_k)
 // and zero elsewhere; the selection has no gradient.
-#include <float.h>
-
 #include "kernels.h"
 #include "common.h"
 
@@ -210,6 +210,10 @@ __device__ inline float key_of(uint32_t u)
     return u == 1u ? NAN : __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
 }
 
+// A NaN key in 64 bits: below every fp32 number, and so is the sum of two of
+// them, which stays above a closed expert's -inf.
+constexpr double kNanKey = -1e300;
+
 // What the selection leaves in lane k < K: slot k's expert (or -1) and logit.
 struct Slot {
     int id;
@@ -270,7 +274,7 @@ __device__ inline Slot select_exact(const RouterArgs &a, int64_t t, int lane, do
     // closed before NaN: a NaN score and a bias of -inf add up to NaN
 #pragma unroll
     for (int i = 0; i < R; ++i)
-        key[i] = closed[i] ? -INFINITY : isnan(key[i]) ? -DBL_MAX : key[i];
+        key[i] = closed[i] ? -INFINITY : isnan(key[i]) ? kNanKey : key[i];
     if (grouped) {
 #pragma unroll
         for (int i = 0; i < R; ++i)
@@ -290,7 +294,11 @@ __device__ inline Slot select_exact(const RouterArgs &a, int64_t t, int lane, do
             b1 = fmax(fmax(b1, o1), fmin(b0, o0));
             b0 = fmax(b0, o0);
         }
-        const double value = g >= a.groups ? -INFINITY : pair ? b0 + b1 : b0;
+        // +inf beside a closed expert would add up to NaN
+        const double value = g >= a.groups          ? -INFINITY
+                             : pair && b1 > -INFINITY ? b0 + b1
+                             : pair                   ? -INFINITY
+                                                      : b0;
         const Bits64 vb(value);
         int rank = 0;
         for (int o = 0; o < a.groups; ++o) {
@@ -306,7 +314,7 @@ __device__ inline Slot select_exact(const RouterArgs &a, int64_t t, int lane, do
             const uint32_t og = a.group_m ? __umulhi(j, a.group_m) : j; // expert / n
             const bool in = j < (uint32_t)E && (kept >> (og * lg & 63) & 1);
             // without a bias, by logit within the groups
-            const double k = a.bias ? key[i] : isnan(l[i]) ? -DBL_MAX : (double)l[i];
+            const double k = a.bias ? key[i] : isnan(l[i]) ? kNanKey : (double)l[i];
             key[i] = in && key[i] > -INFINITY ? k : -INFINITY;
         }
     }
@@ -401,14 +409,14 @@ __device__ inline bool select_fast(const RouterArgs &a, const float *l, float to
     float margin = 0.f;
     if (KIND != BY_LOGIT) {
         float size = 0.f;
-        bool nan = false;
+        bool odd = false; // scores that are no finite numbers are left to select_exact
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             size = fmaxf(size, key[i] != 0u ? fabsf(score[i]) : 0.f);
-            nan |= key[i] != 0u && isnan(score[i]);
+            odd |= key[i] != 0u && !(fabsf(score[i]) < INFINITY);
         }
         margin = key_margin<KIND>(wave_max(size));
-        ok = __ballot(nan) == 0;
+        ok = __ballot(odd) == 0;
     }
     if (grouped) {
         // a group's value: a power of two of lanes scan its experts in LDS
@@ -417,9 +425,7 @@ __device__ inline bool select_fast(const RouterArgs &a, const float *l, float to
 #pragma unroll
         for (int i = 0; i < R; ++i)
             if (lane * R + i < E)
-                keys[lane * R + i] = key[i] == 0u  ? -INFINITY
-                                     : isnan(score[i]) ? -FLT_MAX
-                                                       : score[i];
+                keys[lane * R + i] = key[i] == 0u ? -INFINITY : score[i];
         __builtin_amdgcn_wave_barrier();
         float b0 = -INFINITY, b1 = -INFINITY;
         if (g < a.groups)

@@ -25,6 +25,10 @@ def _scores(l, score):
     return e / e.sum()
 
 
+# a NaN key: below every fp32 number, as is the sum of two, and above a closed expert's -inf
+_NAN_KEY = -1e300
+
+
 def _best(values, n):
     """Indices of the n largest, descending, ties to the lower index."""
     return np.argsort(-values, kind="stable")[:n]
@@ -44,12 +48,14 @@ def router(logits, K, bias=None, score="softmax", renormalize=True, groups=1, to
         key = l.copy() if bias is None else s + np.asarray(bias, np.float64)
         if bias is not None:
             closed |= np.asarray(bias) == -np.inf
-        key = np.where(np.isnan(key), -np.finfo(np.float64).max, key)
+        key = np.where(np.isnan(key), _NAN_KEY, key)
         key[closed] = -np.inf
         if topk_groups < groups:
-            rank = key if bias is not None or group_top == 1 else np.where(closed, -np.inf, s)
+            rank = key if bias is not None or group_top == 1 else np.where(
+                closed, -np.inf, np.where(np.isnan(s), _NAN_KEY, s))
             best = -np.sort(-rank.reshape(groups, -1), axis=1)[:, :group_top]
-            kept = _best(best.sum(1), topk_groups)
+            few = (best == -np.inf).any(1)  # of +inf and a closed expert there is no sum
+            kept = _best(np.where(few, -np.inf, np.where(few[:, None], 0, best).sum(1)), topk_groups)
             mask = np.ones(groups, bool)
             mask[kept] = False
             key[np.repeat(mask, E // groups)] = -np.inf

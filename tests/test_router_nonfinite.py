@@ -83,3 +83,73 @@ def test_random_rows_with_every_kind_of_value(gpu_lib, E, groups, score):
     np.testing.assert_array_equal(ids, rid)
     assert not np.isin(np.nonzero(bias == -INF)[0], ids).any()
     np.testing.assert_array_equal(np.isnan(w), np.isnan(rw))
+
+
+# (score, logits, bias, groups, ids of K = 2 from the best group by the sum of two)
+GROUPS = [
+    # every score is NaN: the group that holds open experts, not the closed one before it
+    ("softmax", [-INF, -INF, NAN, 1], None, 2, [3, 2]),
+    ("softmax", [-INF, -INF, NAN, 1], [0, 0, 0, 0], 2, [2, 3]),
+    ("softmax", [-INF, 5, INF, 1], None, 2, [2, 3]),
+    # two NaNs are above closed experts, below a NaN and a number, and that below two numbers
+    ("sigmoid", [-INF, -INF, NAN, NAN, -INF, -INF], [0] * 6, 3, [2, 3]),
+    ("sigmoid", [NAN, NAN, NAN, -9, -INF, -INF], [0] * 6, 3, [3, 2]),
+    ("sigmoid", [NAN, 99, -9, -9, NAN, NAN], [0] * 6, 3, [2, 3]),
+    # ... however low those are
+    ("sigmoid", [NAN, 1, 0, 0], [0, 0, -3e38, -3e38], 2, [2, 3]),
+    # +inf beside a closed expert is no sum of two; beside a number it is the largest
+    ("sigmoid", [1, -INF, 3, 4], [INF, 0, 0, 0], 2, [3, 2]),
+    ("sigmoid", [3, 4, 1, -INF], [0, 0, INF, 0], 2, [1, 0]),
+    ("sigmoid", [3, 4, 1, 0], [0, 0, INF, 0], 2, [2, 3]),
+    ("sigmoid", [3, 4, 1, NAN], [0, 0, INF, 0], 2, [2, 3]),
+    # one open expert: the lowest value, so that the lower of two such groups is kept
+    ("sigmoid", [-INF, -INF, 9, -INF], None, 2, [-1, -1]),
+    ("sigmoid", [9, -INF, -INF, -INF], None, 2, [0, -1]),
+]
+
+
+def expect_groups(answer, spread=1):
+    """``spread`` closed experts follow each of a group's, which changes no sum and scales the ids."""
+    for score, l, bias, groups, ids in GROUPS:
+        say("[router] groups", score, l, bias)
+        wide = lambda v, fill: [x for y in v for x in [y] + [fill] * (spread - 1)]
+        w, got = answer([wide(l, -INF)], 2, bias=None if bias is None else wide(bias, 0),
+                        score=score, groups=groups, topk_groups=1, group_top=2)
+        assert got.tolist() == [[i * spread if i > 0 else i for i in ids]], (score, l, bias)
+        if score == "softmax":
+            assert np.isnan(w).all()
+
+
+def test_oracle_groups():
+    expect_groups(oracle)
+    expect_groups(oracle, 4)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("spread", [1, 4, 16, 100])
+def test_groups(gpu_lib, spread):
+    """4 and 16: whole lanes of the sixteen, for the cases of two groups."""
+    expect_groups(lambda l, K, **kw: on_gpu(gpu_lib, l, K, **kw), spread)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("with_bias", [True, False], ids=["bias", "plain"])
+@pytest.mark.parametrize("E,groups", [(64, 8), (256, 8), (160, 8), (512, 16)])
+def test_groups_of_random_rows(gpu_lib, E, groups, with_bias, score):
+    say("[router] groups of strewn rows", E, groups, with_bias, score)
+    rng = np.random.default_rng([E, groups, 2])
+    T, K = 300, 6
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    for value in (NAN, INF, -INF, -INF):
+        l[rng.random((T, E)) < 0.9 * rng.random((T, 1)) ** 3] = value
+    bias = None
+    if with_bias:
+        bias = (0.2 * rng.standard_normal(E)).astype(np.float32)
+        bias[rng.random(E) < 0.3] = -INF
+        bias[rng.random(E) < 0.02] = INF
+    kw = dict(score=score, groups=groups, topk_groups=groups // 4, group_top=2)
+    w, ids = on_gpu(gpu_lib, l, K, bias=bias, **kw)
+    rw, rid = oracle(l, K, bias=bias, **kw)
+    np.testing.assert_array_equal(ids, rid)
+    np.testing.assert_array_equal(np.isnan(w), np.isnan(rw))
