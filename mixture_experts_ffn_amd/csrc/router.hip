@@ -362,11 +362,15 @@ __device__ inline Slot select_exact(const RouterArgs &a, int64_t t, int lane, do
 //            the mean |x| <= ln E < 7, reciprocal 2u, product u: below 25u
 //   key:     u size on top
 // and twice that between two keys, which `margin` is: 16u or 56u, and 2u size.
-// Sums of two keys have twice the error.
+// Half the sum of two keys has the same.
 template <int KIND> __device__ inline float key_margin(float size)
 {
     return (KIND == BY_SIGMOID ? 0x1p-20f : 7 * 0x1p-21f) + 0x1p-23f * size;
 }
+
+// A group's value by the sum of two is compared by its half: the sum of two
+// biases of a type's lowest value would be that of a closed group, -inf.
+__device__ inline float half_sum(float x, float y) { return 0.5f * x + 0.5f * y; }
 
 template <int R, int KIND>
 __device__ inline bool select_fast(const RouterArgs &a, const float *l, float top, float total,
@@ -450,7 +454,7 @@ __device__ inline bool select_fast(const RouterArgs &a, const float *l, float to
             join(from(dpp<0x140>(bits(b0))), from(dpp<0x140>(bits(b1))));
         if (lg >= 32)
             join(__shfl_xor(b0, 16), __shfl_xor(b1, 16));
-        const float value = g >= a.groups ? -INFINITY : pair ? b0 + b1 : b0;
+        const float value = g >= a.groups ? -INFINITY : pair ? half_sum(b0, b1) : b0;
         int rank = 0;
         for (int o = 0; o < a.groups; ++o) {
             const float v = lane_value(value, o * lg);
@@ -461,7 +465,7 @@ __device__ inline bool select_fast(const RouterArgs &a, const float *l, float to
         if (sums || pair) {
             const float lo = wave_min(keep ? value : INFINITY);
             const float hi = wave_max(keep ? -INFINITY : value);
-            ok = ok && (!(lo - hi <= 2.f * margin) || hi == -INFINITY);
+            ok = ok && (!(lo - hi <= margin) || hi == -INFINITY);
         }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -745,12 +749,12 @@ __global__ __launch_bounds__(256) void router_rows_kernel(RouterArgs a)
                 join(dpp<0x4E>(__float_as_uint(b0)), dpp<0x4E>(__float_as_uint(b1)));
             if (shift >= 3)
                 join(dpp<0x141>(__float_as_uint(b0)), dpp<0x141>(__float_as_uint(b1)));
-            const float value = pair ? b0 + b1 : b0;
+            const float value = pair ? half_sum(b0, b1) : b0;
             const bool keep = rank_step<1>(value, sub, shift) < a.topk_groups;
             if (sums || pair) {
                 const float lo = -row_max(keep ? -value : -INFINITY);
                 const float hi = row_max(keep ? -INFINITY : value);
-                ok = ok && (!(lo - hi <= 2.f * margin) || hi == -INFINITY);
+                ok = ok && (!(lo - hi <= margin) || hi == -INFINITY);
             }
 #pragma unroll
             for (int i = 0; i < R; ++i)
