@@ -362,7 +362,8 @@ __device__ inline Slot select_exact(const RouterArgs &a, int64_t t, int lane, do
 //            the mean |x| <= ln E < 7, reciprocal 2u, product u: below 25u
 //   key:     u size on top
 // and twice that between two keys, which `margin` is: 16u or 56u, and 2u size.
-// Half the sum of two keys has the same.
+// Half the sum of two keys has the mean of their errors and is rounded itself:
+// 2u size more between two of them.
 template <int KIND> __device__ inline float key_margin(float size)
 {
     return (KIND == BY_SIGMOID ? 0x1p-20f : 7 * 0x1p-21f) + 0x1p-23f * size;
@@ -410,7 +411,7 @@ __device__ inline bool select_fast(const RouterArgs &a, const float *l, float to
         for (int i = 0; i < R; ++i)
             key[i] = order_of(l[i], l[i] == -INFINITY);
     }
-    float margin = 0.f;
+    float margin = 0.f, group_margin = 0.f;
     if (KIND != BY_LOGIT) {
         float size = 0.f;
         bool odd = false; // scores that are no finite numbers are left to select_exact
@@ -419,7 +420,9 @@ __device__ inline bool select_fast(const RouterArgs &a, const float *l, float to
             size = fmaxf(size, key[i] != 0u ? fabsf(score[i]) : 0.f);
             odd |= key[i] != 0u && !(fabsf(score[i]) < INFINITY);
         }
-        margin = key_margin<KIND>(wave_max(size));
+        size = wave_max(size);
+        margin = key_margin<KIND>(size);
+        group_margin = pair ? margin + 0x1p-23f * size : margin;
         ok = __ballot(odd) == 0;
     }
     if (grouped) {
@@ -465,7 +468,7 @@ __device__ inline bool select_fast(const RouterArgs &a, const float *l, float to
         if (sums || pair) {
             const float lo = wave_min(keep ? value : INFINITY);
             const float hi = wave_max(keep ? -INFINITY : value);
-            ok = ok && (!(lo - hi <= margin) || hi == -INFINITY);
+            ok = ok && (!(lo - hi <= group_margin) || hi == -INFINITY);
         }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -724,7 +727,9 @@ __global__ __launch_bounds__(256) void router_rows_kernel(RouterArgs a)
             for (int i = 0; i < R; ++i)
                 key[i] = any_key(l[i], closed[i], sub * R + i);
         }
-        margin = key_margin<KIND>(row_max(size));
+        size = row_max(size);
+        margin = key_margin<KIND>(size);
+        const float group_margin = pair ? margin + 0x1p-23f * size : margin;
         ok = !row_any(odd, lane);
         float b0 = -INFINITY, b1 = -INFINITY;
         if (grouped) {
@@ -754,7 +759,7 @@ __global__ __launch_bounds__(256) void router_rows_kernel(RouterArgs a)
             if (sums || pair) {
                 const float lo = -row_max(keep ? -value : -INFINITY);
                 const float hi = row_max(keep ? -INFINITY : value);
-                ok = ok && (!(lo - hi <= margin) || hi == -INFINITY);
+                ok = ok && (!(lo - hi <= group_margin) || hi == -INFINITY);
             }
 #pragma unroll
             for (int i = 0; i < R; ++i)

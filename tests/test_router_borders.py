@@ -50,3 +50,57 @@ def test_groups_of_the_lowest_and_largest_bias(gpu_lib, E, score):
     ids = check(gpu_lib, rng.standard_normal((40, E)), 2, bias, score=score, groups=4,
                 topk_groups=1, group_top=2)
     assert (ids == [n + 1, n + 2]).all()
+
+
+def group_sums_in_the_wrong_order(rows, E, seed):
+    """Logits [rows, E] and a bias in two groups, the sum of the first group's two keys the larger
+    by less than 2^-24, that fp32 arithmetic may put 2^-17 the other way round.
+
+    Keys lie in [16, 18), where fp32's step is G = 2^-19.  A score of the first group lies just
+    above (n + 1/2) G: a key of even last place goes down by G / 2 from the halfway point, one of
+    odd last place if its score came out a step low.  One of the second group lies just below, and
+    goes up likewise.  The sums, in [32, 36) with a step of 2 G, are then odd multiples of G,
+    halfway again: the first goes down where it is 1 modulo 4, and the second up.
+    """
+    rng = np.random.default_rng(seed)
+    G, n = 2.0 ** -19, E // 2
+    bias = np.zeros(E)
+    bias[[0, 1, n, n + 1]] = [17.25, 16.25, 17.0, 16.5]
+    sign = np.array([1, 1, -1, -1])
+    m = 40 * rows
+    a = rng.integers(int(0.29 / G), int(0.36 / G), (m, 2))
+    shift = rng.integers(-4000, 4000, m)
+    mid = (np.stack([a[:, 0], a[:, 1], a[:, 0] + shift, a[:, 1] - shift], 1) + 0.5) * G
+    s = mid + sign * 0.05 * 2.0 ** -24
+    four = np.log(s / (1 - s)).astype(np.float32)
+    # the fp32 logits' own scores: within 2^-27 of the halfway points, on the right side
+    off = sign * (1 / (1 + np.exp(-four.astype(np.float64))) - mid)
+    good = ((off > 0) & (off < 2.0 ** -27)).all(1)
+    good &= (a.sum(1) + round((bias[0] + bias[1]) / G)) % 4 == 1
+    four = four[good]
+    l = rng.normal(-3, 0.5, (len(four), E)).astype(np.float32)
+    l[:, [0, 1, n, n + 1]] = four
+    return l, bias
+
+
+@pytest.mark.parametrize("E", [16, 18, 64, 512])
+def test_group_sums_next_to_each_other(gpu_lib, E):
+    """E = 16 and 64: sixteen lanes a row; the others: a wave."""
+    l, bias = group_sums_in_the_wrong_order(50000, E, seed=E)
+    ids = check(gpu_lib, l, 2, bias, score="sigmoid", groups=2, topk_groups=1, group_top=2)
+    assert (ids == [0, 1]).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [16.0, 63.9, 300.0, 1e5])
+@pytest.mark.parametrize("E,groups", [(64, 8), (256, 8), (160, 8), (512, 16)])
+def test_sums_of_large_biases(gpu_lib, E, groups, size, score):
+    """Biases far above the scores and a few fp32 steps apart: keys and group sums lie on a coarse
+    grid, and the scores decide."""
+    rng = np.random.default_rng([E, int(size)])
+    step = float(np.spacing(np.float32(size)))
+    bias = size + step * rng.integers(-2, 3, E)
+    l = rng.standard_normal((200, E))
+    for group_top in (1, 2):
+        check(gpu_lib, l, 6, bias, score=score, groups=groups, topk_groups=groups // 2,
+              group_top=group_top)
