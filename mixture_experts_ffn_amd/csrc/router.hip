@@ -355,18 +355,30 @@ __device__ inline Slot select_exact(const RouterArgs &a, int64_t t, int lane, do
 // group) are rounded, and where two that were compared lie closer than the
 // rounding may move them the row is left to select_exact (returns false; with
 // scores spread over (0, 1) about one row in a thousand).  The bound, with
-// u = 2^-24 and every compared value at most `size`:
+// u = 2^-24:
 //   sigmoid: exponential 2u, sum u, reciprocal 2u of a value <= 1: 5u
 //   softmax: exponent |x| u (times p <= e^-|x|: 0.4u), exponential 2u, the
 //            denominator 10u (tree of 16 a lane and six levels) + 2u + u times
 //            the mean |x| <= ln E < 7, reciprocal 2u, product u: below 25u
-//   key:     u size on top
-// and twice that between two keys, which `margin` is: 16u or 56u, and 2u size.
-// Half the sum of two keys has the mean of their errors and is rounded itself:
-// 2u size more between two of them.
-template <int KIND> __device__ inline float key_margin(float size)
+//   key:     u |key| on top
+// so two keys of at most `size` may move 10u or 50u and 2u size against each
+// other; key_margin has 16u or 56u and 3u size, for its own rounding too.  Only
+// neighbours in the order are compared: towards a lower key the distance grows
+// faster than its margin.  `size` is that of the two keys alone, so an expert
+// that a bias of -1e9 switches off costs nothing.
+template <int KIND>
+constexpr float kMargin = KIND == BY_SIGMOID ? 0x1p-20f : 7 * 0x1p-21f;
+template <int KIND> __device__ inline float key_margin(float x, float y)
 {
-    return (KIND == BY_SIGMOID ? 0x1p-20f : 7 * 0x1p-21f) + 0x1p-23f * size;
+    return kMargin<KIND> + 3 * 0x1p-24f * fmaxf(fabsf(x), fabsf(y));
+}
+// How far a group's value may be off: a key, or half the sum of two, b0 >= b1,
+// rounded (2u of the larger), and the rounding of value -+ error where it is
+// compared (u more).  Every kept group has to stay above every other one.
+template <int KIND> __device__ inline float group_error(bool pair, float b0, float b1, float value)
+{
+    const float size = pair ? fmaxf(b0, -b1) : fabsf(b0);
+    return value == -INFINITY ? 0.f : 0.5f * kMargin<KIND> + 0x1p-22f * size;
 }
 
 // A group's value by the sum of two is compared by its half: the sum of two
@@ -411,18 +423,11 @@ __device__ inline bool select_fast(const RouterArgs &a, const float *l, float to
         for (int i = 0; i < R; ++i)
             key[i] = order_of(l[i], l[i] == -INFINITY);
     }
-    float margin = 0.f, group_margin = 0.f;
     if (KIND != BY_LOGIT) {
-        float size = 0.f;
         bool odd = false; // scores that are no finite numbers are left to select_exact
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            size = fmaxf(size, key[i] != 0u ? fabsf(score[i]) : 0.f);
+        for (int i = 0; i < R; ++i)
             odd |= key[i] != 0u && !(fabsf(score[i]) < INFINITY);
-        }
-        size = wave_max(size);
-        margin = key_margin<KIND>(size);
-        group_margin = pair ? margin + 0x1p-23f * size : margin;
         ok = __ballot(odd) == 0;
     }
     if (grouped) {
@@ -466,9 +471,10 @@ __device__ inline bool select_fast(const RouterArgs &a, const float *l, float to
         const bool keep = g < a.groups && rank < a.topk_groups;
         const uint64_t kept = __ballot(keep);
         if (sums || pair) {
-            const float lo = wave_min(keep ? value : INFINITY);
-            const float hi = wave_max(keep ? -INFINITY : value);
-            ok = ok && (!(lo - hi <= group_margin) || hi == -INFINITY);
+            const float err = group_error<KIND>(pair, b0, b1, value);
+            const float lo = wave_min(keep ? value - err : INFINITY);
+            const float hi = wave_max(keep ? -INFINITY : value + err);
+            ok = ok && (lo > hi || hi == -INFINITY);
         }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -478,7 +484,7 @@ __device__ inline bool select_fast(const RouterArgs &a, const float *l, float to
         }
     }
     Slot mine = {-1, -INFINITY};
-    float last = INFINITY;
+    float last = 0.f;
     const int rounds = sums ? K + 1 : K; // with sums, also the first one left out
     for (int k = 0; k < rounds; ++k) {
         uint32_t m = key[0];
@@ -490,7 +496,7 @@ __device__ inline bool select_fast(const RouterArgs &a, const float *l, float to
             break;
         if (sums) {
             const float v = key_of(best);
-            ok = ok && !(last - v <= margin);
+            ok = ok && (k == 0 || last - v > key_margin<KIND>(last, v));
             last = v;
             if (k == K)
                 break;
@@ -665,12 +671,11 @@ __global__ __launch_bounds__(256) void router_rows_kernel(RouterArgs a)
                 }));
         }
     }
-    // keys, and the margin below which fp32 does not order them (select_fast)
+    // keys, and whether fp32 orders them (select_fast)
     const bool grouped = KIND != BY_LOGIT && a.topk_groups < a.groups;
     const bool sums = KIND >= BY_SOFTMAX && a.bias != nullptr;
     const bool pair = KIND >= BY_SOFTMAX && grouped && a.group_top == 2;
     bool ok = true;
-    float margin = 0.f;
     Bits64 key[R];
     if constexpr (KIND == BY_LOGIT) {
 #pragma unroll
@@ -707,13 +712,10 @@ __global__ __launch_bounds__(256) void router_rows_kernel(RouterArgs a)
                 closed[i] = l[i] == -INFINITY;
         }
         // scores that are no finite numbers are left to the exact selection
-        float size = 0.f;
         bool odd = false;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
+        for (int i = 0; i < R; ++i)
             odd |= !(closed[i] || fabsf(v[i]) < INFINITY);
-            size = fmaxf(size, closed[i] ? 0.f : fabsf(v[i]));
-        }
         if constexpr (KIND == BY_LOGIT_GROUPED) {
 #pragma unroll
             for (int i = 0; i < R; ++i)
@@ -727,9 +729,6 @@ __global__ __launch_bounds__(256) void router_rows_kernel(RouterArgs a)
             for (int i = 0; i < R; ++i)
                 key[i] = any_key(l[i], closed[i], sub * R + i);
         }
-        size = row_max(size);
-        margin = key_margin<KIND>(size);
-        const float group_margin = pair ? margin + 0x1p-23f * size : margin;
         ok = !row_any(odd, lane);
         float b0 = -INFINITY, b1 = -INFINITY;
         if (grouped) {
@@ -757,9 +756,10 @@ __global__ __launch_bounds__(256) void router_rows_kernel(RouterArgs a)
             const float value = pair ? half_sum(b0, b1) : b0;
             const bool keep = rank_step<1>(value, sub, shift) < a.topk_groups;
             if (sums || pair) {
-                const float lo = -row_max(keep ? -value : -INFINITY);
-                const float hi = row_max(keep ? -INFINITY : value);
-                ok = ok && (!(lo - hi <= group_margin) || hi == -INFINITY);
+                const float err = group_error<KIND>(pair, b0, b1, value);
+                const float lo = -row_max(keep ? err - value : -INFINITY);
+                const float hi = row_max(keep ? -INFINITY : value + err);
+                ok = ok && (lo > hi || hi == -INFINITY);
             }
 #pragma unroll
             for (int i = 0; i < R; ++i)
@@ -785,7 +785,8 @@ __global__ __launch_bounds__(256) void router_rows_kernel(RouterArgs a)
         const auto number = [](const Bits64 &k) {
             return (float)Bits64(k.lo & 0xE0000000u, k.hi).value();
         };
-        const bool near = !(number(kept) - number(below) > margin);
+        const float x = number(kept), y = number(below);
+        const bool near = !(x - y > key_margin<KIND>(x, y));
         ok = ok && !row_any(sub < a.K && below.hi != kClosedHi && near, lane);
     }
     const int n = (int)(kept.lo & 1023u);

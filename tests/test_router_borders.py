@@ -104,3 +104,53 @@ def test_sums_of_large_biases(gpu_lib, E, groups, size, score):
     for group_top in (1, 2):
         check(gpu_lib, l, 6, bias, score=score, groups=groups, topk_groups=groups // 2,
               group_top=group_top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("off", [-3.0, -1e4, -1e9, -BIG], ids=str)
+@pytest.mark.parametrize("E,groups", [(64, 8), (256, 8), (160, 8), (512, 16)])
+def test_experts_switched_off_by_a_finite_bias(gpu_lib, E, groups, off, score):
+    rng = np.random.default_rng([E, groups])
+    l = rng.standard_normal((200, E))
+    some = 0.1 * rng.standard_normal(E)
+    some[rng.random(E) < 0.2] = off
+    whole = some.copy()  # whole groups, and all but one expert of another
+    whole[:E // 4] = off
+    whole[E // 2:E // 2 + E // groups - 1] = off
+    for bias in (some, whole):
+        for group_top in (1, 2):
+            check(gpu_lib, l, 6, bias, score=score, groups=groups, topk_groups=groups // 2,
+                  group_top=group_top)
+        check(gpu_lib, l, 6, bias, score=score)
+    # fewer experts left than slots: the switched-off ones follow, by their scores where the sum
+    # still shows them, else by their ids
+    bias = np.full(E, off)
+    bias[[3, E - 1]] = 0
+    ids = check(gpu_lib, l, 6, bias, score=score)
+    assert (np.sort(ids[:, :2], axis=1) == [3, E - 1]).all()
+
+
+@pytest.mark.parametrize("E", [256, 320])
+def test_a_finite_mask_costs_no_more_than_a_closed_expert(gpu_lib, E):
+    """A mask of -1e9 or the type's lowest value against one of -inf: about the same time, where
+    rows selected again in 64 bits would take several times as long."""
+    say("[router] time with masked experts", E)
+    l = torch.randn(32768, E, device="cuda")
+    times = {}
+    biases = {}
+    for off in (-INF, -1e9, -BIG):
+        biases[off] = 0.1 * torch.randn(E, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+        biases[off][::9] = off
+    for _ in range(7):
+        for off, bias in biases.items():
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            torch.cuda.synchronize()
+            start.record()
+            for _ in range(10):
+                gpu_lib.moe_ffn_router_fwd(l, 8, bias=bias, score="sigmoid", groups=8, topk_groups=4,
+                                           group_top=2)
+            end.record()
+            end.synchronize()
+            times[off] = min(times.get(off, INF), start.elapsed_time(end) * 100)
+    say("us:", times)
+    assert max(times.values()) < 1.5 * times[-INF]
