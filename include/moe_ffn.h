@@ -423,7 +423,10 @@ int moe_ffn_router_fwd(const moe_ffn_router *r, const void *logits, const float 
  * [T, K] fp32 (moe_ffn_bwd's output, say), the same logits and the ids the
  * forward chose.  The selection is a constant: bias and groups have no
  * gradient and are not read.  A slot whose id is outside [0, E) or whose
- * expert is closed contributes nothing. */
+ * expert's logit is -inf contributes nothing, and no gradient reaches such a
+ * logit.  A NaN or +inf logit makes NaN what depends on it: under softmax
+ * without renormalize every open expert's gradient in a row with a slot,
+ * else those of the row's slots if one of them has it. */
 int moe_ffn_router_bwd(const moe_ffn_router *r, const float *d_topk_weights, const void *logits,
                        const void *topk_ids, void *d_logits, void *stream);
 

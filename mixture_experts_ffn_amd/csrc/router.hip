@@ -907,12 +907,33 @@ __device__ inline SlotGrad slot_grad(const RouterArgs &a, int64_t t, int k, floa
     return s;
 }
 
-// The softmax denominator's parts of a lane's logits, in place of them.
+// The softmax denominator's parts of a lane's logits, in place of them; a closed
+// expert's is -0, which the sum does not see.
 template <int R> __device__ inline void exponentials(float *l, float top)
 {
 #pragma unroll
     for (int i = 0; i < R; ++i)
-        l[i] = l[i] == -INFINITY ? 0.f : expf(l[i] - top);
+        l[i] = l[i] == -INFINITY ? -0.f : expf(l[i] - top);
+}
+// Softmax's gradients g[0, N) from the experts' own parts g and those.  Where the
+// row's values are finite a closed expert's comes out as zero by itself.  Else
+// every open expert takes the formula, one that underflowed to +0 as well, so
+// that a NaN of the row reaches it; closed ones, and rows without a slot, have
+// no gradient.  (With the selection in every row: 32768 x 256 f32 14.7 us, so 14.4.)
+template <int N>
+__device__ inline void dense_grads(const float *part, float inv, float dot, bool any, float *g)
+{
+    if (fabsf(inv * dot) < INFINITY) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            g[i] = part[i] * inv * (g[i] - dot);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const bool closed = __float_as_uint(part[i]) == 0x80000000u;
+            g[i] = closed || !any ? 0.f : part[i] * inv * (g[i] - dot);
+        }
+    }
 }
 
 // N consecutive gradients of token t, from expert j0 on (zeros included).
@@ -983,10 +1004,7 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(RouterArgs a)
             own[i] += lane * R + i == j ? v : 0.f;
     }
     if (dense) {
-        const float inv = 1.f / total;
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-            own[i] = l[i] == 0.f ? 0.f : l[i] * inv * (own[i] - s.dot);
+        dense_grads<R>(l, 1.f / total, s.dot, __ballot(s.id >= 0) != 0, own);
     }
     store_grads<R>(a, t, lane * R, own);
 }
@@ -1056,14 +1074,18 @@ __global__ __launch_bounds__(256) void router_bwd_rows_kernel(RouterArgs a)
     __builtin_amdgcn_wave_barrier();
     if (dense) {
         const float inv = 1.f / total;
+        const bool any = row_any(s.id >= 0, lane);
 #pragma unroll
         for (int i = 0; i < R / V; ++i) {
             Vec v = *reinterpret_cast<const Vec *>(row + i * LINE + sub * V);
+            float g[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float p = l[i * V + j];
-                v[j] = p == 0.f ? 0.f : p * inv * (v[j] - s.dot);
-            }
+            for (int j = 0; j < V; ++j)
+                g[j] = v[j];
+            dense_grads<V>(l + i * V, inv, s.dot, any, g);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                v[j] = g[j];
             *reinterpret_cast<Vec *>(row + i * LINE + sub * V) = v;
         }
         __builtin_amdgcn_wave_barrier();

@@ -117,8 +117,8 @@ def router_grad(d_weights, logits, ids, score="softmax", renormalize=True, scale
             own, size = np.zeros(E), np.zeros(E)
             np.add.at(own, js, g)
             np.add.at(size, js, np.abs(g))
-            d[t] = p * (own - (g * p[js]).sum())
-            mag[t] = p * (size + (np.abs(g) * p[js]).sum())
+            d[t] = np.where(l == -np.inf, 0.0, p * (own - (g * p[js]).sum()))
+            mag[t] = np.where(l == -np.inf, 0.0, p * (size + (np.abs(g) * p[js]).sum()))
     return d, mag
 
 

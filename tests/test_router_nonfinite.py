@@ -153,3 +153,47 @@ def test_groups_of_random_rows(gpu_lib, E, groups, with_bias, score):
     rw, rid = oracle(l, K, bias=bias, **kw)
     np.testing.assert_array_equal(ids, rid)
     np.testing.assert_array_equal(np.isnan(w), np.isnan(rw))
+
+
+# plain softmax, K = 2: (logits, ids, d_topk_weights, which gradients are NaN); the others are 0
+GRADIENTS = [
+    # +inf: the other exponentials underflow to 0, and still depend on it
+    ([INF, 0, 1, -INF], [0, 2], [1, 2], [1, 1, 1, 0]),
+    ([5, INF, -INF, -200], [0, 3], [1, 2], [1, 1, 0, 1]),
+    ([NAN, 0, -300, -INF], [1, 2], [1, 2], [1, 1, 1, 0]),
+    # one NaN gate's gradient reaches an expert whose score is 0
+    ([0, -400, -INF, 1], [0, 3], [NAN, 2], [1, 1, 0, 1]),
+    # no slot: no gradient
+    ([INF, NAN, 1, -INF], [-1, -1], [1, 2], [0, 0, 0, 0]),
+    ([-INF] * 4, [0, -1], [1, 2], [0, 0, 0, 0]),
+]
+
+
+def expect_gradients(grad):
+    for l, ids, dw, nan in GRADIENTS:
+        say("[router] gradient", l, ids)
+        d = grad(np.array([dw], np.float32), np.array([l], np.float32), np.array([ids]))
+        assert np.isnan(d).tolist() == [[bool(n) for n in nan]], (l, ids, d)
+        assert (d[~np.isnan(d)] == 0).all()
+
+
+def test_oracle_gradients():
+    def grad(dw, l, ids):
+        with np.errstate(all="ignore"):
+            return ops.router_grad(dw, l, ids, renormalize=False)[0]
+    expect_gradients(grad)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("pad", [0, 13, 300])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_gradients(gpu_lib, dtype, pad):
+    def grad(dw, l, ids):
+        l = np.pad(l, ((0, 0), (0, pad)), constant_values=-INF)
+        d = gpu_lib.moe_ffn_router_bwd(torch.from_numpy(dw).cuda(),
+                                       torch.from_numpy(l).to(dtype).cuda(),
+                                       torch.from_numpy(ids).cuda(), renormalize=False)
+        d = d.float().cpu().numpy()
+        assert (d[:, l.shape[1] - pad:] == 0).all()
+        return d[:, :l.shape[1] - pad]
+    expect_gradients(grad)
