@@ -766,8 +766,14 @@ def moe_ffn_mxfp4_fwd(x, topk_ids, topk_weights, up: MXFP4Weight, down: MXFP4Wei
 
     ``act`` is the block format ("mxfp4" or "mxfp6") that the token rows and the SwiGLU output
     are quantised to before their product.  ``ws`` may pass a preallocated workspace (uint8, at
-    least ``mxfp4_workspace_size`` bytes)."""
+    least ``mxfp4_workspace_size`` bytes).
+
+    There is no backward pass: with gradients enabled, ``x`` and ``topk_weights`` that require one
+    are refused (call under ``torch.no_grad()``, or with detached tensors)."""
     lib = load_library()
+    if torch.is_grad_enabled() and (x.requires_grad or topk_weights.requires_grad):
+        raise MoEFFNError(3, "the MXFP4 forward has no gradient: x and topk_weights must not "
+                             "require one")
     _require_gpu(x, topk_ids, topk_weights, up.data, down.data, ws)
     _same_device(x, topk_ids, topk_weights, up.data, down.data, ws)
     if x.dim() != 2 or topk_ids.dim() != 2 or topk_ids.shape[0] != x.shape[0]:
