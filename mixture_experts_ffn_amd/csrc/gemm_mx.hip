@@ -140,6 +140,13 @@ __device__ inline __amdgpu_buffer_rsrc_t bytes_at(const void *p, uint32_t n)
                                              __builtin_amdgcn_readfirstlane(n), 0x00020000);
 }
 
+// Byte of a column tile's k-step among an expert's codes: below 4 GiB (the host
+// checks it), not below 2.
+__device__ inline uint32_t code_offset(int tile, int KS, int ks)
+{
+    return ((uint32_t)tile * (uint32_t)KS + (uint32_t)ks) * 1024u;
+}
+
 // The token operand of a tile of rows r0 .. r0 + nr - 1: GEMM1 gathers rows of
 // x (all of them within 4 GiB of codes, which the host checks), GEMM2 reads
 // consecutive rows of act.
@@ -232,7 +239,7 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxGemmArgs a)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 x.w[j][s] = __builtin_amdgcn_raw_buffer_load_b128(
-                    q.wc, wl + s * 1024, q.tile[j] * a.KS * 1024 + p * 2048, 0);
+                    q.wc, wl + s * 1024, code_offset(q.tile[j], a.KS, p * 2), 0);
         }
     };
     auto load_scales = [&](const Place &q, int kc, StreamScales &x) {
@@ -487,7 +494,7 @@ __global__ __launch_bounds__(256, tile_groups(BITS, 32 * TF)) void mx_tile_kerne
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
                     w.c[j][s] = __builtin_amdgcn_raw_buffer_load_b128(
-                        wc, wl + s * 1024, (tl[j] * a.KS + q) * 1024, 0);
+                        wc, wl + s * 1024, code_offset(tl[j], a.KS, q), 0);
         };
         struct S {
             int w[2];
