@@ -479,10 +479,12 @@ __global__ __launch_bounds__(256, tile_groups(BITS, 32 * TF)) void mx_tile_kerne
                     g2l16s(bt + q * 32, src_t[i],
                            (lds_void *)(st + CODES + (wave * NTL + i) * 1024));
         };
-        // scales of the four stages 4g .. 4g + 3
+        // scales of the four stages 4g .. 4g + 3, 16 bytes of a row (past its end: the
+        // last ones again, into the half that is not read any more)
         auto copy_scales = [&](int g) {
+            const int q = min(g, (a.KC - 1) >> 1);
             if (wave < ROWS / 64)
-                g2l16s(bs + g * 16, src_s, (lds_void *)(sscale + (g & 1) * SCALES + wave * 1024));
+                g2l16s(bs + q * 16, src_s, (lds_void *)(sscale + (g & 1) * SCALES + wave * 1024));
         };
         struct W {
             u32x4 c[2][2];
