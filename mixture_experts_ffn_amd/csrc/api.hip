@@ -1353,31 +1353,37 @@ struct MxFwdLayout {
     size_t x_codes, x_tails, x_scales, act_codes, act_tails, act_scales, o, total;
 };
 
-// Rows of an M-tile (MXFP4, GEMM1 + GEMM2 in us; the sides of each rule):
-//  - mean rows per expert up to 20: 32, which pads least (16 x 7168 x 2048, 32
-//    experts, top 8: 127 against 131 with 64; 64 tokens: 134 and 133);
-//  - few tiles of 32 rows in all: 32, where four waves share a tile's
-//    contraction and the chain of a lone tile is shortest (256 x 1024 x 512, 8
-//    experts, top 2: 10 against 13; 1472 such tiles: 13 and 14; 2304: 17 and 15);
-//  - up to 48 mean rows, most experts fit 64 (512 x 2048 x 1408, 64 experts,
-//    top 6: 64 us against 74 with 128; 600 tokens, 56 rows: 77 and 71), and up to
-//    8192 tiles of 32 there are too few of 128 to fill the chip (1024 x 4096 x
-//    1536, 1 expert: 27 against 35; 4096 x 1024 x 1024, 2 experts, top 2: 32 and
-//    29);
-//  - else 128 (256 rows by eight waves: 1028 + 671 us against 1042 + 697 for the
-//    skewed workload with uniform routing, but 411 and 375 for 8192 x 4096 x
-//    1536, 16 experts, top 4).
-int mx_tile_rows(const moe_ffn_problem &p)
+// Rows of an M-tile (whole calls in us inside a replayed graph; the sides of each rule):
+//  - mean rows per expert up to 20: 32, which pads least (GEMM1 + GEMM2 of 16 x 7168
+//    x 2048, 32 experts, top 8: 127 against 131 with 64; 64 tokens: 134 and 133);
+//  - few tiles of 32 rows in all: 32, where four waves share a tile's contraction
+//    and the chain of a lone tile is shortest.  MXFP4 up to 1536 of them: 768 tiles
+//    16.3 against 18.6 with 64, 1280: 24.0 and 29.3, 1408: 22.9 and 23.5, but 1600:
+//    32.1 and 28.0, 1728: 22.6 and 23.2, 2112: 29.3 and 25.0, 2304: 30.4 and 25.6.
+//    MXFP6 up to 512: 416 tiles 21.1 and 22.4, 512: 20.1 and 20.6, 640: 21.1 and 19.8,
+//    768: 26.5 and 23.0, 1280: 37.5 and 33.2;
+//  - up to 48 mean rows, most experts fit 64 (512 x 2048 x 1408, 64 experts, top 6:
+//    GEMMs of 64 us against 74 with 128);
+//  - up to 8192 tiles of 32 there are too few of 128 to fill the chip (4224 tiles:
+//    36.4 against 45.7, 4352: 31.6 and 34.7, 6976: 43.9 and 44.6).  From there to
+//    20000 either may be ahead by up to a tenth (8256: 43.4 and 43.1, 10624: 55.6 and
+//    61.1, 16064: 97 and 91, 17408: 85 and 79), MXFP6 the same;
+//  - else 128 (22080 tiles: 120 and 120, 24256: 86 and 82, 34048: 168 and 148; 256 rows by
+//    eight waves: GEMMs of 1028 + 671 us against 1042 + 697 for the skewed workload
+//    with uniform routing, but 411 and 375 for 8192 x 4096 x 1536, 16 experts, top 4).
+int mx_tile_rows(const moe_ffn_problem &p, int bits)
 {
     const double rows = (double)(p.T * p.K) / (double)p.E;
     const int64_t tiles = moe::max_mtiles_bound(p.T * p.K, (int)p.E, 32) *
                           ((std::max(p.H, p.I) + 31) / 32);
-    return rows <= 20 || tiles <= 1024 ? 32 : rows <= 48 || tiles <= 8192 ? 64 : 128;
+    return rows <= 20 || tiles <= (bits == 4 ? 1536 : 512) ? 32
+           : rows <= 48 || tiles <= 8192                   ? 64
+                                                           : 128;
 }
 
 void mx_fwd_layout(const moe_ffn_problem &p, int bits, MxFwdLayout &L)
 {
-    L.BM = mx_tile_rows(p);
+    L.BM = mx_tile_rows(p, bits);
     L.x = moe::MxDims(p.H, p.I);
     L.act = moe::MxDims(p.I, p.H);
     const int64_t TK = p.T * p.K;

@@ -6,6 +6,7 @@ import torch
 
 from gpu_util import say
 from oracle import operators as ops
+from test_gpu_mxfp4 import check, make
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +75,14 @@ def test_quantised_tokens_past_2_gib(gpu_lib, T, H, E):
         # by a quarter of itself at most, and few do
         d = (y[sl].float() - small).norm() / small.norm()
         assert d.item() < 0.05, d.item()
+
+
+@pytest.mark.parametrize("act", ["mxfp4", "mxfp6"])
+@pytest.mark.parametrize("shape", [
+    (250, 1000, 520, 6, 1), (470, 520, 1000, 1, 1), (490, 520, 1000, 1, 1),  # 448, 512 and 544
+    (333, 1000, 264, 9, 3), (1410, 1000, 72, 3, 1), (1500, 72, 1000, 3, 1),  # 1312, 1536 and 1600
+    (2000, 520, 264, 5, 2), (2100, 1064, 520, 7, 2), (1900, 1064, 520, 7, 2)], ids=str)
+def test_sizes_next_to_the_limits_of_the_tile_heights(gpu_lib, shape, act):
+    """Numbers of 32-row tiles on both sides of the limits (512 and 1536, by format)."""
+    say(f"[mxfp4] ffn {shape} {act}")
+    check(gpu_lib, make(*shape, seed=12), act)
