@@ -402,9 +402,10 @@ __global__ __launch_bounds__(256, tile_groups(BITS, 32 * TF)) void mx_tile_kerne
     const int t1 = (int)((int64_t)total * (xcd + 1) / 8), dt = gridDim.x >> 3;
     // expert-major; inside an expert groups of up to GM M-tiles, column groups
     // outer and M-tiles inner, so that tiles in flight share weights and rows.
-    // GEMM2 with 8: 704 us for 65536 x 2048 x 7168 over 32 experts and 157 for
-    // 32768 x 1536 x 4096 over 16, with 4: 665 and 146 (131072 x 1408 x 2048 over
-    // 8 the other way, 274 and 288); GEMM1 the same within noise
+    // Whole calls, GEMM2 with 4 against 8, three series in turn: 8192 x 7168 x 2048,
+    // 32 experts, top 8: 1875-1886 us and 1888-1903 (Zipf 1869-1879, 1880-1887); x 4096 x
+    // 1536, 16, top 4: 448 and 456; 16384 x 2048 x 1408, 8, top 8: 811 and 813, 64, top 6:
+    // 666 and 669; but 16384 x 4096 x 2048, 8, top 2: 585 and 576
     constexpr int GM = G1 ? 8 : 4;
     struct Place {
         int e, cg, r0, nr; // expert, column group, first row, rows

@@ -236,7 +236,7 @@ struct MxGemmArgs {
     int srow;                        // bytes of a row's scales
     int act_KS, act_srow;            // of GEMM1's output rows
     int max_mtiles;                  // upper bound of the M-tiles
-    int BM;                          // rows of an M-tile: 32, 64, 128 or 256
+    int BM;                          // rows of an M-tile: 32, 64 or 128
 };
 hipError_t launch_mx_gemm(bool g1, int bits, const MxGemmArgs &a, int num_cus, hipStream_t s);
 
