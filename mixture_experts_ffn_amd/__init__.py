@@ -226,12 +226,16 @@ def _check(rc: int):
         raise MoEFFNError(rc, detail)
 
 
-def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
+def _dtype_code_of(dtype) -> int:
+    if dtype == torch.float32:
         return F32
-    if t.dtype == torch.bfloat16:
+    if dtype == torch.bfloat16:
         return BF16
-    raise MoEFFNError(3, f"unsupported dtype {t.dtype}; use float32 or bfloat16")
+    raise MoEFFNError(3, f"unsupported dtype {dtype}; use float32 or bfloat16")
+
+
+def _dtype_code(t: torch.Tensor) -> int:
+    return _dtype_code_of(t.dtype)
 
 
 def _ids_code_of(dtype) -> int:
@@ -706,8 +710,7 @@ class MXFP4Weight:
         return self._nbytes
 
     def _stack(self):
-        return MXFP4Stack(self.E, self.Kd, self.N, self.panels,
-                          F32 if self.dtype == torch.float32 else BF16)
+        return MXFP4Stack(self.E, self.Kd, self.N, self.panels, _dtype_code_of(self.dtype))
 
 
 def _mxfp4_weight_size(stack) -> int:
@@ -736,9 +739,9 @@ def moe_ffn_mxfp4_quantize(weight, panels: int = 1) -> MXFP4Weight:
 def moe_ffn_mxfp4_dequantize(packed: MXFP4Weight):
     """The values [E, Kd, N] that ``packed`` stands for, in the dtype it was packed from."""
     lib = load_library()
+    stack = packed._stack()
     _require_gpu(packed.data)
     dev = packed.data.device
-    stack = packed._stack()
     w = torch.empty((packed.E, packed.Kd, packed.N), dtype=packed.dtype, device=dev)
     _launch(lib.moe_ffn_mxfp4_dequantize, dev, stack, packed.data.data_ptr(),
             packed.data.numel(), w.data_ptr())

@@ -38,3 +38,16 @@ def test_inputs_that_require_a_gradient_on_the_gpu(gpu_lib):
             with mode():
                 y = call("cuda", *grads, packed)
             assert not y.requires_grad and (y > 0).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.uint8, torch.float64, torch.float8_e4m3fn, None])
+def test_packed_weights_of_another_dtype(dtype):
+    """The dtype says what dequantisation writes: one that the library does not know is refused
+    before any pointer is passed on (here: before the CPU tensor is)."""
+    w = m.MXFP4Weight(torch.zeros(1 << 12, dtype=torch.uint8), 1, 32, 32, 1, dtype)
+    for call_it in (lambda: m.moe_ffn_mxfp4_dequantize(w), lambda: w.nbytes):
+        with pytest.raises(m.MoEFFNError) as ei:
+            call_it()
+        assert ei.value.status == 3
+    for known in (torch.float32, torch.bfloat16):
+        assert m.MXFP4Weight(None, 1, 128, 32, 1, known).nbytes == 128 * 32 // 2 + 256
