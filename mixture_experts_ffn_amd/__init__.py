@@ -700,13 +700,15 @@ class MXFP4Weight:
 
     def __init__(self, data, E, Kd, N, panels, dtype):
         self.data, self.E, self.Kd, self.N, self.panels, self.dtype = data, E, Kd, N, panels, dtype
-        self._nbytes = None
+        self._sized = self._nbytes = None
 
     @property
     def nbytes(self) -> int:
         """Bytes that ``data`` must hold."""
-        if self._nbytes is None:
+        sizes = (self.E, self.Kd, self.N, self.panels)
+        if self._sized != sizes:
             self._nbytes = _mxfp4_weight_size(self._stack())
+            self._sized = sizes
         return self._nbytes
 
     def _stack(self):

@@ -51,3 +51,14 @@ def test_packed_weights_of_another_dtype(dtype):
         assert ei.value.status == 3
     for known in (torch.float32, torch.bfloat16):
         assert m.MXFP4Weight(None, 1, 128, 32, 1, known).nbytes == 128 * 32 // 2 + 256
+
+
+def test_the_size_of_packed_weights_follows_their_sizes():
+    """The forward compares it with what the buffer holds."""
+    w = m.MXFP4Weight(None, 1, 128, 32, 1, torch.bfloat16)
+    assert w.nbytes == 128 * 32 // 2 + 256
+    w.E, w.N = 3, 64
+    assert w.nbytes == 3 * 2 * (128 * 32 // 2 + 256)
+    w.Kd = 12
+    with pytest.raises(m.MoEFFNError):
+        w.nbytes
