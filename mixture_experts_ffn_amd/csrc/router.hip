@@ -915,6 +915,9 @@ template <int R> __device__ inline void exponentials(float *l, float top)
     for (int i = 0; i < R; ++i)
         l[i] = l[i] == -INFINITY ? -0.f : expf(l[i] - top);
 }
+// A row of closed experts only, a padded token's, takes the short way below too.
+__device__ inline float inverse_total(float total) { return total == 0.f ? 0.f : 1.f / total; }
+
 // Softmax's gradients g[0, N) from the experts' own parts g and those.  Where the
 // row's values are finite a closed expert's comes out as zero by itself.  Else
 // every open expert takes the formula, one that underflowed to +0 as well, so
@@ -1004,7 +1007,7 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(RouterArgs a)
             own[i] += lane * R + i == j ? v : 0.f;
     }
     if (dense) {
-        dense_grads<R>(l, 1.f / total, s.dot, __ballot(s.id >= 0) != 0, own);
+        dense_grads<R>(l, inverse_total(total), s.dot, __ballot(s.id >= 0) != 0, own);
     }
     store_grads<R>(a, t, lane * R, own);
 }
@@ -1073,7 +1076,7 @@ __global__ __launch_bounds__(256) void router_bwd_rows_kernel(RouterArgs a)
     }
     __builtin_amdgcn_wave_barrier();
     if (dense) {
-        const float inv = 1.f / total;
+        const float inv = inverse_total(total);
         const bool any = row_any(s.id >= 0, lane);
 #pragma unroll
         for (int i = 0; i < R / V; ++i) {
