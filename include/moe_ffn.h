@@ -481,6 +481,126 @@ int moe_ffn_mxfp4_fwd(const moe_ffn_problem *p, int32_t act_format, const void *
                       const void *down_packed, void *y, void *ws, size_t ws_bytes, uint32_t flags,
                       void *stream);
 
+/* ---- the experts' products on their own ----------------------------------------- */
+
+/* Products of row groups with their own weight matrices, for experts that the
+ * fused layer does not cover (another activation, an adapter, rows that the
+ * caller dispatched itself): with offsets [E + 1] as moe_ffn_route writes them,
+ * group e owns the rows offsets[e] <= m < offsets[e + 1], and
+ *
+ *     y[m]  = x[m] · W[e]              x [M, Kd], y [M, N]
+ *     dx[m] = dy[m] · W[e]^T
+ *     dW[e] = Σ_{m in group e} x[m]^T dy[m]   (zeros for an empty group)
+ *
+ * with W[e] = weight[e] of weight [E, Kd, N], or weight[e]^T of [E, N, Kd]
+ * with `transposed`.  Sums are fp32; outputs are rounded once to the dtype.
+ * Rows outside every group (before offsets[0], from offsets[E] on) give zeros
+ * in y and dx.  The offsets are read on the device and never lead outside the
+ * M rows: what counts is the running maximum of the offsets, each held to
+ * [0, M].
+ *
+ * Limits: 0 <= M <= 2^30, 1 <= E <= 1024, Kd and N positive multiples of 8,
+ * Kd·N < 2^31, x_stride >= Kd and a multiple of 8.  weight, y, dy, dx and dW
+ * are dense; x's rows are x_stride elements apart. */
+typedef struct {
+    int64_t M, E, Kd, N;
+    int64_t x_stride;      /* elements from one row of x to the next */
+    int32_t dtype;         /* MOE_FFN_F32 or MOE_FFN_BF16: x, weight, y and the gradients */
+    int32_t offsets_dtype; /* MOE_FFN_I32 or MOE_FFN_I64 */
+    int32_t transposed;    /* 1: weight is [E, N, Kd] */
+} moe_ffn_grouped;
+
+/* Workspace of either call below.  Pure host function. */
+int moe_ffn_grouped_workspace_size(const moe_ffn_grouped *g, size_t *ws_bytes);
+int moe_ffn_grouped_mm(const moe_ffn_grouped *g, const void *x, const void *weight,
+                       const void *offsets, void *y, void *ws, size_t ws_bytes, void *stream);
+/* dx [M, Kd] (dense) and d_weight (the shape of weight), overwritten; either may
+ * be NULL, and then is not computed, nor is its other input read (weight for
+ * dx, x for d_weight), which may be NULL too. */
+int moe_ffn_grouped_mm_bwd(const moe_ffn_grouped *g, const void *dy, const void *x,
+                           const void *weight, const void *offsets, void *dx, void *d_weight,
+                           void *ws, size_t ws_bytes, void *stream);
+
+/* ---- products in 8-bit integers --------------------------------------------------- */
+
+/* int8 with one fp32 scale for each token row and for each weight column: a
+ * vector v (a token's row; a weight's column along the contraction) has
+ *
+ *     scale = max|v| / 127 (rounded to fp32),
+ *     code  = v / scale rounded to nearest, ties to even, held to [-127, 127];
+ *
+ * a vector of zeros has scale 0; one with a NaN or an infinity has scale NaN
+ * and codes 0, so that its row or column of every product is NaN and no other. */
+
+/* A stack of E weight matrices [Kd, N] (Kd the contraction length), row-major,
+ * in `dtype` (F32 or BF16); `panels` equal column panels are laid out apart, 2
+ * for moe_ffn_int8_fwd's up_proj_weight (gate and up), else 1.  Limits:
+ * 1 <= E <= 1024, Kd % 8 == 0, Kd <= 131072 (the products' sums are exact in 32
+ * bits), N % (8 · panels) == 0, Kd · N < 2^31. */
+typedef struct {
+    int64_t E, Kd, N;
+    int32_t panels;
+    int32_t dtype;
+} moe_ffn_int8_weight;
+
+/* Bytes of the packed form, an opaque buffer for the calls below (pure host
+ * function). */
+int moe_ffn_int8_weight_size(const moe_ffn_int8_weight *w, size_t *packed_bytes);
+/* weight [E, Kd, N] -> packed (16-byte aligned, of packed_bytes at least). */
+int moe_ffn_int8_quantize(const moe_ffn_int8_weight *w, const void *weight, void *packed,
+                          size_t packed_bytes, void *stream);
+/* Weights that are quantised already: codes [E, Kd, N] int8 (any of -128..127)
+ * and scales [E, N] fp32 -> packed.  dtype is only the one that
+ * moe_ffn_int8_dequantize gives back. */
+int moe_ffn_int8_pack(const moe_ffn_int8_weight *w, const void *codes, const float *scales,
+                      void *packed, size_t packed_bytes, void *stream);
+/* The values code · scale that `packed` stands for -> weight [E, Kd, N], rounded
+ * to dtype. */
+int moe_ffn_int8_dequantize(const moe_ffn_int8_weight *w, const void *packed, size_t packed_bytes,
+                            void *weight, void *stream);
+
+/* Token rows x [M, Kd] -> codes [M, row_bytes] int8 (row_bytes from the query:
+ * Kd rounded up to 64, the rest zeros) and scales [M].  Limits as for the
+ * weights; x_stride >= Kd and a multiple of 8; codes 16-byte aligned. */
+typedef struct {
+    int64_t M, Kd;
+    int64_t x_stride; /* elements from one row of x to the next */
+    int32_t dtype;    /* MOE_FFN_F32 or MOE_FFN_BF16 */
+} moe_ffn_int8_rows;
+int moe_ffn_int8_row_bytes(int64_t Kd, int64_t *row_bytes);
+int moe_ffn_int8_quantize_rows(const moe_ffn_int8_rows *r, const void *x, void *codes,
+                               float *scales, void *stream);
+
+/* y[m, n] = (Σ_k codes[m, k] · code_e[k, n]) · scales[m] · scale_e[n] for the rows
+ * of group e (rows of no group: zeros), [M, N] in out_dtype; the sum is exact.
+ * offsets [E + 1] as above, or NULL with E = 1: every row.  The weight's dtype
+ * is not read.  Limits: those of the weight; one matrix's packed weights below
+ * 4 GiB; 0 <= M <= 2^30. */
+typedef struct {
+    moe_ffn_int8_weight weight;
+    int64_t M;
+    int32_t offsets_dtype; /* MOE_FFN_I32 or MOE_FFN_I64 */
+    int32_t out_dtype;     /* MOE_FFN_F32 or MOE_FFN_BF16 */
+} moe_ffn_int8_product;
+/* Workspace.  Pure host function. */
+int moe_ffn_int8_mm_workspace_size(const moe_ffn_int8_product *p, size_t *ws_bytes);
+int moe_ffn_int8_mm(const moe_ffn_int8_product *p, const void *codes, const float *scales,
+                    const void *packed, size_t packed_bytes, const void *offsets, void *y,
+                    void *ws, size_t ws_bytes, void *stream);
+
+/* moe_ffn_fwd (saved = NULL) on int8 weights: up_packed of {E, H, 2I, 2 panels},
+ * down_packed of {E, I, H, 1 panel}.  The token rows, and act = silu(gate) ⊙ up
+ * (in fp32), are quantised row by row before their product; an expert's output
+ * row is rounded to bf16 before the combine, as in moe_ffn_fwd.  dtype must be
+ * BF16 and Is 0; the flags MOE_FFN_CHECK_IDS and MOE_FFN_CHECK_STATUS apply,
+ * others are rejected with MOE_FFN_ERR_SHAPE, and so are calls of 2^24 tokens or
+ * more, H or I above 131072, and those whose token codes (T · H bytes, H rounded
+ * up to 64) or one expert's packed weights reach 4 GiB. */
+int moe_ffn_int8_workspace_size(const moe_ffn_problem *p, uint32_t flags, size_t *ws_bytes);
+int moe_ffn_int8_fwd(const moe_ffn_problem *p, const void *x, const void *topk_ids,
+                     const float *topk_weights, const void *up_packed, const void *down_packed,
+                     void *y, void *ws, size_t ws_bytes, uint32_t flags, void *stream);
+
 /* ---- status and measurement helpers ---------------------------------------- */
 
 /* Synchronises `stream`, then reads the device status word that the last

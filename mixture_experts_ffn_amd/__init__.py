@@ -17,6 +17,13 @@ Public API (names follow the C ABI of ``include/moe_ffn.h``):
 * ``moe_ffn_mxfp4_quantize(weight, panels)`` -> packed 4-bit expert weights
   (``moe_ffn_mxfp4_dequantize`` gives the values back)
 * ``moe_ffn_mxfp4_fwd(x, topk_ids, topk_weights, up, down, act="mxfp4")`` -> ``y``
+* ``moe_ffn_grouped_mm(x, weight, offsets)`` autograd-aware product of row groups with their own
+  weights (``moe_ffn_grouped_mm_fwd`` and ``moe_ffn_grouped_mm_bwd`` are its two halves)
+* ``moe_ffn_int8_quantize(weight, panels)`` -> packed int8 weights with a scale for each column
+  (``moe_ffn_int8_pack`` takes codes and scales, ``moe_ffn_int8_dequantize`` gives the values back)
+* ``moe_ffn_int8_quantize_rows(x)`` -> int8 token rows with a scale for each
+* ``moe_ffn_int8_mm(x, weight, offsets=None)`` -> their product, dense or by groups
+* ``moe_ffn_int8_fwd(x, topk_ids, topk_weights, up, down)`` -> ``y`` of the layer on int8 weights
 """
 
 from __future__ import annotations
@@ -63,6 +70,22 @@ __all__ = [
     "moe_ffn_mxfp4_dequantize",
     "mxfp4_workspace_size",
     "moe_ffn_mxfp4_fwd",
+    "Grouped",
+    "grouped_workspace_size",
+    "moe_ffn_grouped_mm_fwd",
+    "moe_ffn_grouped_mm_bwd",
+    "moe_ffn_grouped_mm",
+    "MoEGroupedMMFunction",
+    "Int8Weight",
+    "Int8Rows",
+    "moe_ffn_int8_quantize",
+    "moe_ffn_int8_pack",
+    "moe_ffn_int8_dequantize",
+    "moe_ffn_int8_quantize_rows",
+    "int8_mm_workspace_size",
+    "moe_ffn_int8_mm",
+    "int8_workspace_size",
+    "moe_ffn_int8_fwd",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -123,6 +146,26 @@ class Router(ctypes.Structure):
 class MXFP4Stack(ctypes.Structure):
     _fields_ = [("E", ctypes.c_int64), ("Kd", ctypes.c_int64), ("N", ctypes.c_int64),
                 ("panels", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class Grouped(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("E", ctypes.c_int64), ("Kd", ctypes.c_int64),
+                ("N", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("offsets_dtype", ctypes.c_int32), ("transposed", ctypes.c_int32)]
+
+
+class Int8Stack(ctypes.Structure):
+    _fields_ = MXFP4Stack._fields_
+
+
+class Int8RowsShape(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("Kd", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
+
+
+class Int8Product(ctypes.Structure):
+    _fields_ = [("weight", Int8Stack), ("M", ctypes.c_int64), ("offsets_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32)]
 
 
 class FwdStageLayout(ctypes.Structure):
@@ -192,6 +235,19 @@ def load_library():
             "moe_ffn_mxfp4_dequantize": [ctypes.POINTER(MXFP4Stack), vp, sz, vp, vp],
             "moe_ffn_mxfp4_workspace_size": [pp, i32, u32, psz],
             "moe_ffn_mxfp4_fwd": [pp, i32, vp, vp, vp, vp, vp, vp, vp, sz, u32, vp],
+            "moe_ffn_grouped_workspace_size": [ctypes.POINTER(Grouped), psz],
+            "moe_ffn_grouped_mm": [ctypes.POINTER(Grouped), vp, vp, vp, vp, vp, sz, vp],
+            "moe_ffn_grouped_mm_bwd": [ctypes.POINTER(Grouped), vp, vp, vp, vp, vp, vp, vp, sz, vp],
+            "moe_ffn_int8_weight_size": [ctypes.POINTER(Int8Stack), psz],
+            "moe_ffn_int8_quantize": [ctypes.POINTER(Int8Stack), vp, vp, sz, vp],
+            "moe_ffn_int8_pack": [ctypes.POINTER(Int8Stack), vp, vp, vp, sz, vp],
+            "moe_ffn_int8_dequantize": [ctypes.POINTER(Int8Stack), vp, sz, vp, vp],
+            "moe_ffn_int8_row_bytes": [ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)],
+            "moe_ffn_int8_quantize_rows": [ctypes.POINTER(Int8RowsShape), vp, vp, vp, vp],
+            "moe_ffn_int8_mm_workspace_size": [ctypes.POINTER(Int8Product), psz],
+            "moe_ffn_int8_mm": [ctypes.POINTER(Int8Product), vp, vp, vp, sz, vp, vp, vp, sz, vp],
+            "moe_ffn_int8_workspace_size": [pp, u32, psz],
+            "moe_ffn_int8_fwd": [pp, vp, vp, vp, vp, vp, vp, vp, sz, u32, vp],
             "moe_ffn_read_status": [vp, vp, ctypes.POINTER(ctypes.c_int32)],
             "moe_ffn_event_create": [ctypes.POINTER(ctypes.c_void_p)],
             "moe_ffn_event_destroy": [vp],
@@ -799,6 +855,310 @@ def moe_ffn_mxfp4_fwd(x, topk_ids, topk_weights, up: MXFP4Weight, down: MXFP4Wei
         ws = torch.empty(mxfp4_workspace_size(prob, act, flags), dtype=torch.uint8, device=dev)
     y = torch.empty_like(x)
     _launch(lib.moe_ffn_mxfp4_fwd, dev, prob, _act_code(act), x.data_ptr(), topk_ids.data_ptr(),
+            topk_weights.data_ptr(), up.data.data_ptr(), down.data.data_ptr(), y.data_ptr(),
+            ws.data_ptr(), ws.nbytes, flags)
+    return (y, ws) if return_ws else y
+
+
+def _require_rows(name, t):
+    """A matrix on the GPU whose rows may be strided: the elements from one row to the next."""
+    if not t.is_cuda:
+        raise MoEFFNError(1, "all tensors must be on the GPU (no CPU fallback exists)")
+    if t.dim() != 2:
+        raise MoEFFNError(2, f"expected {name} with two dimensions")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise MoEFFNError(4, f"a row of {name} must be consecutive")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _require_offsets(offsets, E):
+    _require_gpu(offsets)
+    code = _ids_code_of(offsets.dtype)
+    if offsets.shape != (E + 1,):
+        raise MoEFFNError(2, f"expected offsets [E + 1] = [{E + 1}], got {tuple(offsets.shape)}")
+    return code
+
+
+def _workspace(ws, size, device, *args):
+    """The caller's workspace, or one of ``size(*args)`` bytes."""
+    if ws is None:
+        return torch.empty(size(*args), dtype=torch.uint8, device=device)
+    _require_gpu(ws)
+    if ws.device != device:
+        raise MoEFFNError(1, f"the workspace is on {ws.device}, the call on {device}")
+    return ws
+
+
+def _grouped(x, weight, offsets, transposed) -> Grouped:
+    stride = _require_rows("x", x)
+    _require_gpu(weight)
+    if weight.dim() != 3:
+        raise MoEFFNError(2, "expected weight [E, Kd, N], or [E, N, Kd] with transposed")
+    E = weight.shape[0]
+    code = _require_offsets(offsets, E)
+    _same_device(x, weight, offsets)
+    Kd, N = (weight.shape[2], weight.shape[1]) if transposed else weight.shape[1:]
+    if x.shape[1] != Kd:
+        raise MoEFFNError(2, f"x has {x.shape[1]} columns, weight contracts {Kd}")
+    if x.dtype != weight.dtype:
+        raise MoEFFNError(3, "x and weight must share one dtype")
+    return Grouped(x.shape[0], E, Kd, N, stride, _dtype_code(x), code, 1 if transposed else 0)
+
+
+def grouped_workspace_size(grouped: Grouped) -> int:
+    ws = ctypes.c_size_t()
+    _check(load_library().moe_ffn_grouped_workspace_size(ctypes.byref(grouped), ctypes.byref(ws)))
+    return ws.value
+
+
+def moe_ffn_grouped_mm_fwd(x, weight, offsets, *, transposed: bool = False, ws=None):
+    """y [M, N]: rows offsets[e] <= m < offsets[e + 1] of x [M, Kd] times weight[e] of weight
+    [E, Kd, N] (or, with ``transposed``, weight[e] transposed of [E, N, Kd]); rows outside every
+    group are zero (include/moe_ffn.h, moe_ffn_grouped_mm).
+
+    float32 or bfloat16; the rows of ``x`` may be strided, by a multiple of 8 elements.
+    ``offsets`` [E + 1] are int32 or int64 and stay on the device.  ``ws`` may pass a preallocated
+    workspace (uint8, at least ``grouped_workspace_size`` bytes)."""
+    lib = load_library()
+    g = _grouped(x, weight, offsets, transposed)
+    dev = x.device
+    ws = _workspace(ws, grouped_workspace_size, dev, g)
+    y = torch.empty((g.M, g.N), dtype=x.dtype, device=dev)
+    _launch(lib.moe_ffn_grouped_mm, dev, g, x.data_ptr(), weight.data_ptr(), offsets.data_ptr(),
+            y.data_ptr(), ws.data_ptr(), ws.nbytes)
+    return y
+
+
+def moe_ffn_grouped_mm_bwd(dy, x, weight, offsets, *, transposed: bool = False,
+                           need_dx: bool = True, need_dw: bool = True, ws=None):
+    """(dx [M, Kd], d_weight) of ``moe_ffn_grouped_mm_fwd`` from dy [M, N]; None for what is not
+    needed.  A row outside every group has dx zero and no part in d_weight; an empty group's
+    d_weight is zero."""
+    lib = load_library()
+    g = _grouped(x, weight, offsets, transposed)
+    _require_gpu(dy)
+    _same_device(x, dy)
+    if dy.shape != (g.M, g.N) or dy.dtype != x.dtype:
+        raise MoEFFNError(2, f"expected dy [{g.M}, {g.N}] in the dtype of x")
+    dev = x.device
+    ws = _workspace(ws, grouped_workspace_size, dev, g)
+    dx = torch.empty((g.M, g.Kd), dtype=x.dtype, device=dev) if need_dx else None
+    dw = torch.empty_like(weight) if need_dw else None
+    _launch(lib.moe_ffn_grouped_mm_bwd, dev, g, dy.data_ptr(), x.data_ptr(), weight.data_ptr(),
+            offsets.data_ptr(), _ptr(dx), _ptr(dw), ws.data_ptr(), ws.nbytes)
+    return dx, dw
+
+
+class MoEGroupedMMFunction(torch.autograd.Function):
+    """Autograd wrapper of the grouped product: differentiable in x and weight."""
+
+    @staticmethod
+    def forward(ctx, x, weight, offsets, transposed):
+        ctx.save_for_backward(x, weight, offsets)
+        ctx.transposed = transposed
+        return moe_ffn_grouped_mm_fwd(x, weight, offsets, transposed=transposed)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight, offsets = ctx.saved_tensors
+        dx, dw = moe_ffn_grouped_mm_bwd(dy.contiguous(), x, weight, offsets,
+                                        transposed=ctx.transposed,
+                                        need_dx=ctx.needs_input_grad[0],
+                                        need_dw=ctx.needs_input_grad[1])
+        return dx, dw, None, None
+
+
+def moe_ffn_grouped_mm(x, weight, offsets, *, transposed: bool = False):
+    """``moe_ffn_grouped_mm_fwd``, differentiable in x and weight."""
+    return MoEGroupedMMFunction.apply(x, weight, offsets, transposed)
+
+
+class Int8Weight:
+    """Weights [E, Kd, N] packed by ``moe_ffn_int8_quantize`` or ``moe_ffn_int8_pack``: ``data``
+    (uint8, the library's layout), the sizes, the number of column panels and the dtype that
+    ``moe_ffn_int8_dequantize`` gives back."""
+
+    def __init__(self, data, E, Kd, N, panels, dtype):
+        self.data, self.E, self.Kd, self.N, self.panels, self.dtype = data, E, Kd, N, panels, dtype
+        self._sized = self._nbytes = None
+
+    @property
+    def nbytes(self) -> int:
+        """Bytes that ``data`` must hold."""
+        sizes = (self.E, self.Kd, self.N, self.panels)
+        if self._sized != sizes:
+            self._nbytes = _int8_weight_size(self._stack())
+            self._sized = sizes
+        return self._nbytes
+
+    def _stack(self):
+        return Int8Stack(self.E, self.Kd, self.N, self.panels, _dtype_code_of(self.dtype))
+
+
+class Int8Rows:
+    """Token rows in int8: ``codes`` [M, Kd rounded up to 64] (int8, zeros behind Kd), ``scales``
+    [M] (float32), ``Kd`` and the dtype of the rows they came from."""
+
+    def __init__(self, codes, scales, Kd, dtype):
+        self.codes, self.scales, self.Kd, self.dtype = codes, scales, Kd, dtype
+
+
+def _int8_weight_size(stack) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().moe_ffn_int8_weight_size(ctypes.byref(stack), ctypes.byref(n)))
+    return n.value
+
+
+def _no_gradient(what, *ts):
+    if torch.is_grad_enabled() and any(t.requires_grad for t in ts):
+        raise MoEFFNError(3, f"{what} has no gradient: its inputs must not require one")
+
+
+def moe_ffn_int8_quantize(weight, panels: int = 1) -> Int8Weight:
+    """Pack weights [E, Kd, N] (float32 or bfloat16; [Kd, N] is a stack of one) as int8 with a
+    scale for each column: max|w| / 127 along Kd, codes rounded to nearest even.
+
+    up_proj_weight [E, H, 2I] of ``moe_ffn_int8_fwd`` takes ``panels`` 2, all else 1."""
+    lib = load_library()
+    _require_gpu(weight)
+    if weight.dim() not in (2, 3):
+        raise MoEFFNError(2, "expected weight [E, Kd, N] or [Kd, N]")
+    E, Kd, N = weight.shape if weight.dim() == 3 else (1, *weight.shape)
+    stack = Int8Stack(E, Kd, N, panels, _dtype_code(weight))
+    dev = weight.device
+    data = torch.empty(_int8_weight_size(stack), dtype=torch.uint8, device=dev)
+    _launch(lib.moe_ffn_int8_quantize, dev, stack, weight.data_ptr(), data.data_ptr(),
+            data.numel())
+    return Int8Weight(data, E, Kd, N, panels, weight.dtype)
+
+
+def moe_ffn_int8_pack(codes, scales, panels: int = 1, dtype=torch.bfloat16) -> Int8Weight:
+    """Pack weights that are int8 already: ``codes`` [E, Kd, N] (int8) and ``scales`` [E, N]
+    (float32), or [Kd, N] and [N].  ``dtype`` is the one that ``moe_ffn_int8_dequantize`` gives
+    back."""
+    lib = load_library()
+    _require_gpu(codes, scales)
+    _same_device(codes, scales)
+    if codes.dim() not in (2, 3):
+        raise MoEFFNError(2, "expected codes [E, Kd, N] or [Kd, N]")
+    if codes.dtype != torch.int8 or scales.dtype != torch.float32:
+        raise MoEFFNError(3, "codes must be int8 and scales float32")
+    if scales.shape != codes.shape[:-2] + codes.shape[-1:]:
+        raise MoEFFNError(2, "expected one scale for each column: [E, N], or [N] for [Kd, N]")
+    E, Kd, N = codes.shape if codes.dim() == 3 else (1, *codes.shape)
+    stack = Int8Stack(E, Kd, N, panels, _dtype_code_of(dtype))
+    dev = codes.device
+    data = torch.empty(_int8_weight_size(stack), dtype=torch.uint8, device=dev)
+    _launch(lib.moe_ffn_int8_pack, dev, stack, codes.data_ptr(), scales.data_ptr(),
+            data.data_ptr(), data.numel())
+    return Int8Weight(data, E, Kd, N, panels, dtype)
+
+
+def moe_ffn_int8_dequantize(packed: Int8Weight):
+    """The values code * scale [E, Kd, N] that ``packed`` stands for, rounded to its dtype."""
+    lib = load_library()
+    stack = packed._stack()
+    _require_gpu(packed.data)
+    dev = packed.data.device
+    w = torch.empty((packed.E, packed.Kd, packed.N), dtype=packed.dtype, device=dev)
+    _launch(lib.moe_ffn_int8_dequantize, dev, stack, packed.data.data_ptr(), packed.data.nbytes,
+            w.data_ptr())
+    return w
+
+
+def moe_ffn_int8_quantize_rows(x) -> Int8Rows:
+    """Token rows [M, Kd] (float32 or bfloat16; rows may be strided) as int8 with a scale for each
+    row: max|x| / 127, codes rounded to nearest even."""
+    lib = load_library()
+    stride = _require_rows("x", x)
+    _no_gradient("the int8 quantisation", x)
+    M, Kd = x.shape
+    row = ctypes.c_int64()
+    _check(lib.moe_ffn_int8_row_bytes(Kd, ctypes.byref(row)))
+    dev = x.device
+    codes = torch.empty((M, row.value), dtype=torch.int8, device=dev)
+    scales = torch.empty(M, dtype=torch.float32, device=dev)
+    _launch(lib.moe_ffn_int8_quantize_rows, dev, Int8RowsShape(M, Kd, stride, _dtype_code(x)),
+            x.data_ptr(), codes.data_ptr(), scales.data_ptr())
+    return Int8Rows(codes, scales, Kd, x.dtype)
+
+
+def int8_mm_workspace_size(product: Int8Product) -> int:
+    ws = ctypes.c_size_t()
+    _check(load_library().moe_ffn_int8_mm_workspace_size(ctypes.byref(product), ctypes.byref(ws)))
+    return ws.value
+
+
+def moe_ffn_int8_mm(x, weight: Int8Weight, offsets=None, *, out_dtype=None, ws=None):
+    """y [M, N] of int8 token rows and int8 weights: the exact integer sum times the row's and the
+    column's scale, in ``out_dtype`` (float32 or bfloat16; by default the dtype of the rows).
+
+    ``x`` is an ``Int8Rows``, or a matrix [M, Kd] that is quantised first.  With ``offsets``
+    [E + 1] (int32 or int64, on the device) rows offsets[e] <= m < offsets[e + 1] meet matrix e and
+    rows outside every group are zero; without, the one matrix of a stack of one meets all rows.
+    ``ws`` may pass a preallocated workspace (uint8, at least ``int8_mm_workspace_size`` bytes).
+    There is no backward pass."""
+    lib = load_library()
+    rows = x if isinstance(x, Int8Rows) else moe_ffn_int8_quantize_rows(x)
+    _require_gpu(rows.codes, rows.scales, weight.data)
+    _same_device(rows.codes, rows.scales, weight.data, offsets)
+    if rows.Kd != weight.Kd:
+        raise MoEFFNError(2, f"the rows have {rows.Kd} values, the weight contracts {weight.Kd}")
+    M = rows.codes.shape[0]
+    if (rows.codes.dtype != torch.int8 or rows.scales.dtype != torch.float32
+            or rows.scales.shape != (M,) or rows.codes.shape[1:] != (-(-rows.Kd // 64) * 64,)):
+        raise MoEFFNError(2, "the rows do not hold int8 codes [M, Kd rounded up to 64] and float32 "
+                             "scales [M]")
+    code = I32 if offsets is None else _require_offsets(offsets, weight.E)
+    dtype = rows.dtype if out_dtype is None else out_dtype
+    p = Int8Product(weight._stack(), M, code, _dtype_code_of(dtype))
+    dev = weight.data.device
+    ws = _workspace(ws, int8_mm_workspace_size, dev, p)
+    y = torch.empty((M, weight.N), dtype=dtype, device=dev)
+    _launch(lib.moe_ffn_int8_mm, dev, p, rows.codes.data_ptr(), rows.scales.data_ptr(),
+            weight.data.data_ptr(), weight.data.nbytes, _ptr(offsets), y.data_ptr(), ws.data_ptr(),
+            ws.nbytes)
+    return y
+
+
+def int8_workspace_size(problem: Problem, flags: int = 0) -> int:
+    ws = ctypes.c_size_t()
+    _check(load_library().moe_ffn_int8_workspace_size(ctypes.byref(problem), flags,
+                                                      ctypes.byref(ws)))
+    return ws.value
+
+
+def moe_ffn_int8_fwd(x, topk_ids, topk_weights, up: Int8Weight, down: Int8Weight, *,
+                     check_ids: bool = False, ws=None, return_ws: bool = False, flags: int = 0):
+    """y [T, H] of the layer on packed int8 weights (inference; include/moe_ffn.h,
+    moe_ffn_int8_fwd): token rows and the SwiGLU output are quantised row by row.
+
+    ``ws`` may pass a preallocated workspace (uint8, at least ``int8_workspace_size`` bytes).
+    There is no backward pass: with gradients enabled, ``x`` and ``topk_weights`` that require one
+    are refused."""
+    lib = load_library()
+    _no_gradient("the int8 forward", x, topk_weights)
+    _require_gpu(x, topk_ids, topk_weights, up.data, down.data, ws)
+    _same_device(x, topk_ids, topk_weights, up.data, down.data, ws)
+    if x.dim() != 2 or topk_ids.dim() != 2 or topk_ids.shape[0] != x.shape[0]:
+        raise MoEFFNError(2, "expected x [T, H] and topk_ids [T, K]")
+    if topk_weights.dtype != torch.float32 or topk_weights.shape != topk_ids.shape:
+        raise MoEFFNError(3, "topk_weights must be float32 with the shape of topk_ids")
+    T, H = x.shape
+    E, I = down.E, down.Kd
+    if (up.E, up.Kd, up.N, up.panels) != (E, H, 2 * I, 2) or (down.N, down.panels) != (H, 1):
+        raise MoEFFNError(2, "expected up packed from [E, H, 2I] with 2 panels and down from "
+                             "[E, I, H] with 1")
+    if up.data.nbytes < up.nbytes or down.data.nbytes < down.nbytes:
+        raise MoEFFNError(5, "packed weights shorter than their sizes need")
+    prob = Problem(T, H, I, E, topk_ids.shape[1], _dtype_code(x), _ids_code(topk_ids))
+    flags |= CHECK_IDS if check_ids else 0
+    dev = x.device
+    if ws is None:
+        ws = torch.empty(int8_workspace_size(prob, flags), dtype=torch.uint8, device=dev)
+    y = torch.empty_like(x)
+    _launch(lib.moe_ffn_int8_fwd, dev, prob, x.data_ptr(), topk_ids.data_ptr(),
             topk_weights.data_ptr(), up.data.data_ptr(), down.data.data_ptr(), y.data_ptr(),
             ws.data_ptr(), ws.nbytes, flags)
     return (y, ws) if return_ws else y

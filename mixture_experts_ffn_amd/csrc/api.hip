@@ -18,6 +18,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "host.h"
 #include "kernels.h"
 #include "moe_ffn.h"
 #include "mx.h"
@@ -33,7 +34,11 @@ thread_local char g_err[512];
 // epoch stamped into every saved context (distinct per forward that saves one)
 std::atomic<uint64_t> g_epoch{1};
 
-int fail(int status, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+} // namespace
+
+namespace moe {
+namespace host {
+
 int fail(int status, const char *fmt, ...)
 {
     va_list ap;
@@ -48,17 +53,7 @@ int hip_fail(hipError_t err, const char *what)
     return fail(MOE_FFN_ERR_HIP, "%s: %s", what, hipGetErrorString(err));
 }
 
-#define HIP_TRY(expr, what)                                                                        \
-    do {                                                                                           \
-        hipError_t e_ = (expr);                                                                    \
-        if (e_ != hipSuccess)                                                                      \
-            return hip_fail(e_, what);                                                             \
-    } while (0)
-
-constexpr size_t kAlign = 256;
-inline size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
-size_t elem_size(int dtype) { return dtype == MOE_FFN_BF16 ? 2 : 4; }
+void clear_error() { g_err[0] = 0; }
 
 int validate_problem(const moe_ffn_problem *p)
 {
@@ -94,13 +89,7 @@ int validate_problem(const moe_ffn_problem *p)
     return MOE_FFN_OK;
 }
 
-// Shared-expert chunks S = Is / I; the plan covers E + S experts and
-// T*K + S*T permuted rows (the shared rows after the routed ones).
-int nshared(const moe_ffn_problem &p) { return (int)(p.Is / p.I); }
-
-bool aligned16(const void *ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
-
-int check_ptr(const void *ptr, const char *name, size_t align = 16)
+int check_ptr(const void *ptr, const char *name, size_t align)
 {
     if (!ptr)
         return fail(MOE_FFN_ERR_NULL, "%s is NULL", name);
@@ -111,10 +100,10 @@ int check_ptr(const void *ptr, const char *name, size_t align = 16)
 
 // The current device must be a gfx950 GPU.  Cached per device ordinal, with
 // its compute-unit count (the persistent kernels size their grids by it).
-int g_num_cus[64] = {0};
-int g_clock_khz[64] = {0}; // rate of the device's constant wall clock (s_memrealtime)
+static int g_num_cus[64] = {0};
+static int g_clock_khz[64] = {0}; // rate of the device's constant wall clock (s_memrealtime)
 
-int check_device(int *num_cus = nullptr, int *clock_khz = nullptr)
+int check_device(int *num_cus, int *clock_khz)
 {
     static std::mutex mu;
     static signed char known[64] = {0}; // 0 unknown, 1 ok, -1 not gfx950
@@ -146,6 +135,19 @@ int check_device(int *num_cus = nullptr, int *clock_khz = nullptr)
         *clock_khz = g_clock_khz[dev];
     return MOE_FFN_OK;
 }
+
+} // namespace host
+} // namespace moe
+
+using namespace moe::host;
+
+namespace {
+
+// Shared-expert chunks S = Is / I; the plan covers E + S experts and
+// T*K + S*T permuted rows (the shared rows after the routed ones).
+int nshared(const moe_ffn_problem &p) { return (int)(p.Is / p.I); }
+
+bool aligned16(const void *ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
 
 // Tile height of the forward's M-tiles from the mean rows per expert.  bf16
 // with whole tiles (the fast path): 64 for small segments (decode, bound by
@@ -423,11 +425,6 @@ int side_stream(SideStream *out, std::unique_lock<std::mutex> *enqueue_lock)
     *out = g_side[dev];
     *enqueue_lock = std::unique_lock<std::mutex>(g_side_enqueue[dev]);
     return MOE_FFN_OK;
-}
-
-template <typename P> P *at(void *base, size_t off)
-{
-    return reinterpret_cast<P *>(static_cast<char *>(base) + off);
 }
 
 void record(const moe_ffn_stage_events *ev, int stage, bool begin, hipStream_t s)

@@ -15,6 +15,11 @@
 //   B5  dW2[e] = Σ_p act_g[p]^T dY[t_p]     M = I, N = H, K = rows of e
 //   B7  dW1[e] = Σ_p x[t_p]^T dh[p]         M = H, N = 2I, K = rows of e
 //
+// and the weight gradient of the grouped products, whose rows lie in group order
+// already (F2 and B4 serve their other two contractions):
+//
+//   GW  dW[e]  = Σ_p a[p]^T b[p]            M, N = columns of a and b, K = rows of e
+//
 // Operand layouts in memory decide the LDS layout and the fragment read:
 //  * KROW: the operand's M (or N) rows are contiguous along K (x, act, dY,
 //    dh rows; W2 rows for B2; W1 rows for B4).  LDS tile [R][BK] with the
@@ -68,7 +73,7 @@ template <int PIECES> __device__ __forceinline__ int krow_piece(int r, int q)
 // A page of zeros that out-of-problem pieces copy from.
 __device__ __attribute__((aligned(256))) const uint32_t kZeroPage[64] = {0};
 
-enum Kind { F1 = 0, F2 = 1, B2 = 2, B4 = 3, B5 = 4, B7 = 5 };
+enum Kind { F1 = 0, F2 = 1, B2 = 2, B4 = 3, B5 = 4, B7 = 5, GW = 6 };
 enum Lay { KROW = 0, KCOL = 1 };
 
 template <int KIND> struct KindTraits;
@@ -96,6 +101,10 @@ template <> struct KindTraits<B5> {
 };
 template <> struct KindTraits<B7> {
     static constexpr bool TOKEN_M = false, A_GATHER = true, B_GATHER = false, PAIRED = false;
+    static constexpr int ALAY = KCOL, BLAY = KCOL;
+};
+template <> struct KindTraits<GW> {
+    static constexpr bool TOKEN_M = false, A_GATHER = false, B_GATHER = false, PAIRED = false;
     static constexpr int ALAY = KCOL, BLAY = KCOL;
 };
 
@@ -626,7 +635,7 @@ __device__ __forceinline__ void epilogue_staged(const EngineArgs &a, const TileI
     bf16 *out = a.C;
     int64_t ld = a.ldc;
     int cjump = 0;
-    if constexpr (KIND == B5 || KIND == B7) {
+    if constexpr (KIND == B5 || KIND == B7 || KIND == GW) {
         // dW[e] [M, N]; a shared-expert chunk writes its rows (B5) or its gate
         // and up column chunks (B7) of the shared gradient
         const bool shd = a.Cs && t.e >= a.Er;
@@ -669,7 +678,7 @@ __device__ __forceinline__ void epilogue_staged(const EngineArgs &a, const TileI
                 // by the layer: stored with the non-temporal hint, they do not
                 // displace cached operands (forward + backward step -1 %, the
                 // following step's GEMM1 454 -> 438 us)
-                if constexpr (KIND == B5 || KIND == B7)
+                if constexpr (KIND == B5 || KIND == B7 || KIND == GW)
                     __builtin_nontemporal_store(v, dst);
                 else
                     *dst = v;
@@ -987,8 +996,10 @@ void engine_feature_tiling(int kind, int M, int N, int num_cus, int *tiles_per_e
 {
     using namespace eng;
     // the weight-gradient kinds launch with 128-row feature tiles (launch_engine)
-    const int out_n = kind == ENG_B5 ? Cfg<B5, 128, 2>::OUT_N : Cfg<B7, 128, 2>::OUT_N;
-    const int wgpc = kind == ENG_B5 ? Shape<B5>::WGPC : Shape<B7>::WGPC;
+    const int out_n = kind == ENG_B5 ? Cfg<B5, 128, 2>::OUT_N
+                      : kind == ENG_B7 ? Cfg<B7, 128, 2>::OUT_N
+                                       : Cfg<GW, 128, 2>::OUT_N;
+    const int wgpc = kind == ENG_B5 ? Shape<B5>::WGPC : kind == ENG_B7 ? Shape<B7>::WGPC : Shape<GW>::WGPC;
     *tiles_per_expert = ((M + 127) / 128) * ((N + out_n - 1) / out_n);
     *wg_per_xcd = (num_cus + 7) / 8 * wgpc;
 }
@@ -1008,9 +1019,10 @@ hipError_t launch_engine(int kind, int BM, const EngineArgs &args, int num_cus, 
     case F1: return BM == 64 ? launch<F1, 64, 1>(a, num_cus, stream) : launch<F1, 128, 1>(a, num_cus, stream);
     case F2: return BM == 64 ? launch<F2, 64, 1>(a, num_cus, stream) : launch<F2, 128, 1>(a, num_cus, stream);
     case B2: return launch<B2, 128, 2>(a, num_cus, stream);
-    case B4: return launch<B4, 128, 2>(a, num_cus, stream);
+    case B4: return BM == 64 ? launch<B4, 64, 1>(a, num_cus, stream) : launch<B4, 128, 2>(a, num_cus, stream);
     case B5: return launch<B5, 128, 2>(a, num_cus, stream);
     case B7: return launch<B7, 128, 2>(a, num_cus, stream);
+    case GW: return launch<GW, 128, 2>(a, num_cus, stream);
     default: return hipErrorInvalidValue;
     }
 }

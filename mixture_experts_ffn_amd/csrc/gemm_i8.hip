@@ -1,0 +1,540 @@
+// gemm_i8.hip — grouped GEMMs on int8 codes with token and column scales.
+//
+//   h[p, n] = (sum_k codes[p, k] . code_e[k, n]) scale[p] scale_e[n]
+//
+// with the sum exact in 32 bits (Kd <= 131072) and one of three epilogues: the
+// product itself in bf16 or fp32, or act = silu(gate) * up of the two panels in
+// fp32, the rows gathered by the routing.  act stays in fp32 because it is
+// quantised to 8 bits next, row by row, which needs the whole row's maximum: a
+// rounding to bf16 first would move one code in ten by a step.
+//
+// All run on the 32 x 32 x 32 matrix instruction with the weights as the first
+// operand (its rows are weight columns) and the token rows as the second: a lane
+// then holds 16 weight columns of one token, in groups of four neighbours.
+#include "i8.h"
+#include "kernels.h"
+#include "tile_common.h"
+
+namespace moe {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+__device__ inline i32x16 i8_mma(u32x4 w, u32x4 a, i32x16 c)
+{
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, w),
+                                                 __builtin_bit_cast(i32x4, a), c, 0, 0, 0);
+}
+
+// `n` bytes from p as a buffer: loads take a scalar base, a scalar offset and
+// one register of lane offset, and past the end they return zero.
+__device__ inline __amdgpu_buffer_rsrc_t i8_bytes(const void *p, uint32_t n)
+{
+    const uint64_t b = (uint64_t)(uintptr_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc((void *)(uintptr_t)((uint64_t)hi << 32 | lo), 0,
+                                             __builtin_amdgcn_readfirstlane(n), 0x00020000);
+}
+
+// Byte of a column tile's k-step among an expert's codes: below 4 GiB (the host
+// checks it), not below 2.
+__device__ inline uint32_t i8_code_offset(int tile, int KS, int ks)
+{
+    return ((uint32_t)tile * (uint32_t)KS + (uint32_t)ks) * 1024u;
+}
+
+// M-tiles: of the tables, or, without them, of one group of all rows.
+struct I8Tile {
+    int e, r0, end, mt0, mts; // group, its first row and end, its first M-tile and their number
+};
+__device__ inline int i8_mtiles(const I8GemmArgs &a)
+{
+    return a.mtile_off ? tile::ldc(a.mtile_off, a.E) : a.max_mtiles;
+}
+__device__ inline I8Tile i8_group(const I8GemmArgs &a, int m)
+{
+    using namespace tile;
+    if (!a.mtile_off)
+        return {0, 0, (int)a.M, 0, a.max_mtiles};
+    const int e = ldc(a.mtile_expert, m), mt0 = ldc(a.mtile_off, e);
+    return {e, ldc(a.offsets, e), ldc(a.offsets, e + 1), mt0, ldc(a.mtile_off, e + 1) - mt0};
+}
+
+// Four neighbouring columns of a token from their sums.
+__device__ inline f32x4 i8_scaled(const i32x16 &acc, int q, float row, f32x4 col)
+{
+    f32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = (float)acc[4 * q + i] * row * col[i];
+    return v;
+}
+__device__ inline f32x4 i8_swiglu(f32x4 g, f32x4 u)
+{
+    f32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = silu_f(g[i]) * u[i];
+    return v;
+}
+
+// First output column of a column tile of the product (which counts through the
+// panels), and the end of its panel.
+struct I8Columns {
+    int first, end;
+};
+__device__ inline I8Columns i8_columns(const I8GemmArgs &a, int tile)
+{
+    const int panel = tile >= a.NT ? 1 : 0, pc = a.N / a.panels;
+    return {panel * pc + (tile - panel * a.NT) * 32, (panel + 1) * pc};
+}
+
+// Weight streaming kernel.  A tile is 32 token rows of one group times four column
+// tiles (SwiGLU: two gate and the same two up tiles); the four waves split the
+// contraction, each streaming its part of the weights from memory straight into
+// registers, and are summed through LDS at the end.  What a wave needs is in
+// flight two k-step pairs (16 KB of weights) ahead, across the end of a tile too.
+struct I8Pair2 {
+    u32x4 w[4][2]; // [tile][k-step]
+    u32x4 a[2];
+};
+
+template <int KIND> __global__ __launch_bounds__(256, 2) void i8_stream_kernel(I8GemmArgs a)
+{
+    using namespace tile;
+    constexpr bool G1 = KIND == I8_SWIGLU;
+    __shared__ i32x4 red[4][3][4][64]; // [tile][other wave][register / 4][lane]
+    const int lane = threadIdx.x & 63;
+    const int wave = uni(threadIdx.x >> 6);
+    const int h = lane >> 5;
+    constexpr int PER = G1 ? 2 : 4; // column tiles of a panel
+    const int ntt = G1 ? a.NT : a.NT * a.panels;
+    const int ncg = (ntt + PER - 1) / PER;
+    const int64_t total = (int64_t)i8_mtiles(a) * ncg;
+    // an XCD's workgroups (blockIdx % 8) take a contiguous part of the tiles, so
+    // a group's token rows stay in one L2
+    const int xcd = blockIdx.x & 7;
+    const int64_t t1 = total * (xcd + 1) / 8;
+    // the wave's k-step pairs [p0, p1)
+    const int KP = a.KS >> 1;
+    const int p0 = KP * wave / 4, p1 = KP * (wave + 1) / 4;
+
+    struct Place {
+        int e, cg, nr, row;
+        uint32_t ao;                    // this lane's token row
+        float as;                       // and its scale
+        __amdgpu_buffer_rsrc_t ac, wc;  // token rows, the group's weights
+        int tile[4];                    // column tiles, counted from there
+    };
+    const int64_t etiles = (int64_t)a.NT * a.panels; // of a group's weights
+    auto place = [&](int64_t t, Place &q) {
+        const int m = (int)(t / ncg);
+        q.cg = uni((int)(t - (int64_t)m * ncg));
+        const I8Tile g = i8_group(a, m);
+        q.e = g.e;
+        const int r0 = g.r0 + (m - g.mt0) * 32;
+        q.nr = min(32, g.end - r0);
+        const int r = min(lane & 31, q.nr - 1);
+        q.row = r0 + r;
+        const int64_t arow = G1 ? a.sorted_slot[q.row] / a.topk : q.row;
+        q.as = a.ascales[arow];
+        const int64_t first = G1 ? 0 : r0, n = G1 ? a.M : q.nr;
+        q.ac = i8_bytes(a.acodes + first * (a.KS * 32), (uint32_t)(n * (a.KS * 32)));
+        q.ao = (uint32_t)(arow - first) * (uint32_t)(a.KS * 32) + h * 16;
+        q.wc = i8_bytes(a.wcodes + g.e * etiles * a.KS * 1024, (uint32_t)(etiles * a.KS * 1024));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            q.tile[j] = min(q.cg * PER + (G1 ? j >> 1 : j), ntt - 1) + (G1 ? (j & 1) * a.NT : 0);
+    };
+    const uint32_t wl = lane * 16;
+    auto load = [&](const Place &q, int p, I8Pair2 &x) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            x.a[s] = __builtin_amdgcn_raw_buffer_load_b128(q.ac, q.ao + s * 32, p * 64, 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                x.w[j][s] = __builtin_amdgcn_raw_buffer_load_b128(
+                    q.wc, wl + s * 1024, i8_code_offset(q.tile[j], a.KS, p * 2), 0);
+        }
+    };
+    i32x16 acc[4];
+    auto compute = [&](const I8Pair2 &x) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[j] = i8_mma(x.w[j][s], x.a[s], acc[j]);
+    };
+
+    int64_t t = total * xcd / 8 + (blockIdx.x >> 3);
+    if (t >= t1)
+        return;
+    Place q;
+    I8Pair2 x, y;
+    auto first = [&] {
+        place(t, q);
+        if (p0 < p1)
+            load(q, p0, x);
+    };
+    first();
+    while (true) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                acc[j][i] = 0;
+        for (int p = p0; p < p1; p += 2) {
+            if (p + 1 < p1)
+                load(q, p + 1, y);
+            compute(x);
+            if (p + 1 < p1) {
+                if (p + 2 < p1)
+                    load(q, p + 2, x);
+                compute(y);
+            }
+        }
+        const int cg = q.cg, nr = q.nr, row = q.row, e = q.e;
+        const float as = q.as;
+        t += gridDim.x >> 3;
+        if (t < t1)
+            first();
+        // wave w sums tile w
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j != wave) {
+                const int slot = wave < j ? wave : wave - 1;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    red[j][slot][q][lane] =
+                        i32x4{acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]};
+            }
+        __syncthreads();
+        i32x16 sum;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j == wave)
+                sum = acc[j];
+#pragma unroll
+        for (int s = 0; s < 3; ++s)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const i32x4 v = red[wave][s][q][lane];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sum[4 * q + i] += v[i];
+            }
+        const bool live = (lane & 31) < nr;
+        // this wave's column tile
+        const int ct = min(cg * PER + (G1 ? wave >> 1 : wave), ntt - 1) + (G1 ? (wave & 1) * a.NT : 0);
+        const float *cs = a.wscales + (e * etiles + ct) * 32 + 4 * h;
+        f32x4 out[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            out[q] = i8_scaled(sum, q, as, *reinterpret_cast<const f32x4 *>(cs + 8 * q));
+        if constexpr (G1) {
+            __syncthreads();
+            if (wave & 1) { // the up tile goes to the wave of its gate tile
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    red[wave][0][q][lane] = __builtin_bit_cast(i32x4, out[q]);
+            }
+            __syncthreads();
+            if (!(wave & 1)) {
+                const int c = cg * 2 + (wave >> 1);
+                float *orow = static_cast<float *>(a.out) + (int64_t)row * a.N;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f32x4 up = __builtin_bit_cast(f32x4, red[wave + 1][0][q][lane]);
+                    const int col = c * 32 + 8 * q + 4 * h;
+                    if (live && c < a.NT && col < a.N)
+                        *reinterpret_cast<f32x4 *>(orow + col) = i8_swiglu(out[q], up);
+                }
+            }
+        } else {
+            const I8Columns cols = i8_columns(a, ct);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int col = cols.first + 8 * q + 4 * h;
+                if (live && cg * PER + wave < ntt && col < cols.end) {
+                    if constexpr (KIND == I8_F32) {
+                        *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + (int64_t)row * a.N +
+                                                   col) = out[q];
+                    } else {
+                        const bf16x4 o = {(bf16)out[q][0], (bf16)out[q][1], (bf16)out[q][2],
+                                          (bf16)out[q][3]};
+                        *reinterpret_cast<bf16x4 *>(static_cast<bf16 *>(a.out) + (int64_t)row * a.N +
+                                                    col) = o;
+                    }
+                }
+            }
+        }
+        if (t >= t1)
+            return;
+        __syncthreads();
+    }
+}
+
+// Tile kernel.  A tile is 32 TF token rows of one group times eight column tiles,
+// two a wave: SwiGLU a gate tile and the up tile of the same columns (so the
+// epilogue stays in the wave), else two neighbours.  The weights go from memory
+// straight into registers, since the waves share none; the token rows, which
+// all four waves read, are copied into a ring of LDS stages of two k-steps, 64
+// bytes a row, swizzled so that the 32 rows of a fragment read spread over all banks.
+template <int KIND, int TF>
+__global__ __launch_bounds__(256, 2) void i8_tile_kernel(I8GemmArgs a)
+{
+    using namespace tile;
+    constexpr bool G1 = KIND == I8_SWIGLU;
+    constexpr int ROWS = TF * 32, STAGE = ROWS * 64, RING = 4;
+    constexpr int NC = TF / 2; // token copies of a wave and stage
+    constexpr int NL = 4;      // weight loads of a wave and stage
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[RING * STAGE];
+    const int wave = uni(threadIdx.x >> 6);
+    constexpr int PER = G1 ? 4 : 8; // column tiles of a panel
+    const int ntt = G1 ? a.NT : a.NT * a.panels;
+    const int ncg = (ntt + PER - 1) / PER;
+    const int KP = a.KS >> 1; // stages
+    const int total = uni(i8_mtiles(a)) * ncg; // below 2^31 (checked at launch)
+    const int64_t etiles = (int64_t)a.NT * a.panels;
+    const int xcd = blockIdx.x & 7;
+    const int t1 = (int)((int64_t)total * (xcd + 1) / 8), dt = gridDim.x >> 3;
+    // group-major; inside a group groups of up to GM M-tiles, column groups outer
+    // and M-tiles inner, so that tiles in flight share weights and rows
+    constexpr int GM = 8;
+    struct Place {
+        int e, cg, r0, nr; // group, column group, first row, rows
+    };
+    auto place = [&](int t) {
+        Place q;
+        const I8Tile g = i8_group(a, uni((int)((unsigned)t / (unsigned)ncg)));
+        q.e = uni(g.e);
+        const unsigned local = t - g.mt0 * ncg;
+        const int grp = uni(local / (unsigned)(GM * ncg));
+        const unsigned gm = min(g.mts - grp * GM, GM);
+        const unsigned rr = local - grp * GM * ncg;
+        q.cg = uni(rr / gm);
+        const int mt = grp * GM + (int)(rr - q.cg * gm);
+        q.r0 = uni(g.r0 + mt * ROWS);
+        q.nr = uni(min(ROWS, g.end - q.r0));
+        return q;
+    };
+    int t = (int)((int64_t)total * xcd / 8) + (blockIdx.x >> 3);
+    if (t >= t1)
+        return;
+    Place next = place(t);
+    for (; t < t1; t += dt) {
+        // what depends on the lane alone is formed anew for each tile: kept
+        // across the tiles it would not fit beside the accumulators
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));
+        const int h = lane >> 5, fr = lane & 31;
+        const int e = next.e, cg = next.cg, r0 = next.r0, nr = next.nr;
+
+        // a copy moves 1024 bytes, 16 rows.  Byte offsets of this lane's sources
+        // from a scalar base (SwiGLU: all of x's codes, below 4 GiB; else the tile's
+        // first row).
+        const int64_t first = G1 ? 0 : r0;
+        auto row_of = [&](int r) -> uint32_t {
+            r = min(r, nr - 1);
+            return G1 ? a.sorted_slot[r0 + r] / a.topk : r;
+        };
+        const uint8_t *const bc = a.acodes + first * (a.KS * 32);
+        uint32_t src[NC];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int r = (wave * NC + i) * 16 + (lane >> 2);
+            src[i] = row_of(r) * (uint32_t)(a.KS * 32) + aswz<4>(r, lane & 3) * 16;
+        }
+        const auto wc = i8_bytes(a.wcodes + e * etiles * a.KS * 1024, (uint32_t)(etiles * a.KS * 1024));
+        int tl[2]; // the wave's column tiles
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            tl[j] = uni(min(cg * PER + (G1 ? wave : 2 * wave + j), ntt - 1) + (G1 ? j * a.NT : 0));
+        const uint32_t wl = lane * 16;
+        // copies of stage p (past the end: of the last one, into a stage that is not read again)
+        auto copy = [&](int p) {
+            unsigned char *st = smem + (p & (RING - 1)) * STAGE;
+            const int q = min(p, KP - 1);
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                g2l16s(bc + q * 64, src[i], (lds_void *)(st + (wave * NC + i) * 1024));
+        };
+        struct W {
+            u32x4 c[2][2];
+        };
+        auto load_w = [&](int p, W &w) {
+            const int q = min(p, KP - 1) * 2;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    w.c[j][s] = __builtin_amdgcn_raw_buffer_load_b128(
+                        wc, wl + s * 1024, i8_code_offset(tl[j], a.KS, q), 0);
+        };
+        i32x16 acc[2][TF];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int f = 0; f < TF; ++f)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    acc[j][f][i] = 0;
+        auto compute = [&](int p, const W &w) {
+            const unsigned char *st = smem + (p & (RING - 1)) * STAGE;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int f = 0; f < TF; ++f) {
+                    const int r = f * 32 + fr;
+                    const u32x4 av =
+                        *reinterpret_cast<const u32x4 *>(st + r * 64 + aswz<4>(r, 2 * s + h) * 16);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[j][f] = i8_mma(w.c[j][s], av, acc[j][f]);
+                }
+        };
+        W w0, w1;
+        copy(0);
+        load_w(0, w0);
+        copy(1);
+        load_w(1, w1);
+        next = place(min(t + dt, t1 - 1)); // under the first loads
+        wait_vm<NC + 2 * NL>();
+        lds_barrier();
+        // Stage p: its copies and weights were issued two stages ago.  The
+        // copies of p + 2 precede the weights' loads of p + 2, so waiting for
+        // all but the youngest operations covers the copies of p + 1.
+        constexpr int YOUNG = 2 * NL + NC;
+        int p = 0;
+        for (; p + 2 <= KP; p += 2) {
+            copy(p + 2);
+            compute(p, w0);
+            load_w(p + 2, w0);
+            wait_vm<YOUNG>();
+            lds_barrier();
+            copy(p + 3);
+            compute(p + 1, w1);
+            load_w(p + 3, w1);
+            wait_vm<YOUNG>();
+            lds_barrier();
+        }
+        if (p < KP)
+            compute(p, w0);
+        wait_vm<0>();
+        lds_barrier();
+        // the last barrier: every wave is past its reads, so the next tile may copy.
+        // The 32 columns of a column tile are turned in LDS, 32 rows at a time, so
+        // that a store instruction writes whole lines: of four row fragments the
+        // turn lies in the ring's last two stages, which the next tile's copies
+        // reach after a barrier; of two it takes the whole ring.
+        unsigned char *const turn = smem + (TF == 4 ? 2 * STAGE : 0) + wave * 4096;
+        f32x4 cs[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                cs[j][q] = *reinterpret_cast<const f32x4 *>(a.wscales + (e * etiles + tl[j]) * 32 +
+                                                            8 * q + 4 * h);
+#pragma unroll
+        for (int f = 0; f < TF; ++f) {
+            const float rs = a.ascales[first + row_of(f * 32 + fr)];
+            if constexpr (KIND == I8_BF16) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x4 v = i8_scaled(acc[j][f], q, rs, cs[j][q]);
+                        const bf16x4 o = {(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
+                        *reinterpret_cast<bf16x4 *>(turn + fr * 128 + aswz<8>(fr, j * 4 + q) * 16 +
+                                                    h * 8) = o;
+                    }
+                asm volatile("" ::: "memory"); // a wave's LDS operations complete in order
+                const int part = lane & 7, j = part >> 2; // 16 bytes: eight columns
+                const I8Columns cols = i8_columns(a, tl[0] + j);
+                const int col = cols.first + (part & 3) * 8;
+                const bool in = cg * PER + 2 * wave + j < ntt && col < cols.end;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int rl = i * 8 + (lane >> 3), r = f * 32 + rl;
+                    const u32x4 v =
+                        *reinterpret_cast<const u32x4 *>(turn + rl * 128 + aswz<8>(rl, part) * 16);
+                    if (r < nr && in) {
+                        u32x4 *dst = reinterpret_cast<u32x4 *>(static_cast<bf16 *>(a.out) +
+                                                               (int64_t)(r0 + r) * a.N + col);
+                        if (a.stream_out)
+                            __builtin_nontemporal_store(v, dst);
+                        else
+                            *dst = v;
+                    }
+                }
+                asm volatile("" ::: "memory");
+            } else {
+#pragma unroll
+                for (int j = 0; j < (G1 ? 1 : 2); ++j) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        f32x4 v = i8_scaled(acc[j][f], q, rs, cs[j][q]);
+                        if constexpr (G1)
+                            v = i8_swiglu(v, i8_scaled(acc[1][f], q, rs, cs[1][q]));
+                        *reinterpret_cast<f32x4 *>(turn + fr * 128 + aswz<8>(fr, 2 * q + h) * 16) = v;
+                    }
+                    asm volatile("" ::: "memory");
+                    const int part = lane & 7; // 16 bytes: four columns
+                    const I8Columns cols = G1 ? I8Columns{tl[0] * 32, a.N} : i8_columns(a, tl[j]);
+                    const int col = cols.first + part * 4;
+                    const bool in = cg * PER + (G1 ? wave : 2 * wave + j) < ntt && col < cols.end;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int rl = i * 8 + (lane >> 3), r = f * 32 + rl;
+                        const u32x4 v =
+                            *reinterpret_cast<const u32x4 *>(turn + rl * 128 + aswz<8>(rl, part) * 16);
+                        if (r < nr && in) {
+                            u32x4 *dst = reinterpret_cast<u32x4 *>(static_cast<float *>(a.out) +
+                                                                   (int64_t)(r0 + r) * a.N + col);
+                            if (a.stream_out)
+                                __builtin_nontemporal_store(v, dst);
+                            else
+                                *dst = v;
+                        }
+                    }
+                    asm volatile("" ::: "memory");
+                }
+            }
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F); // LDS only: writes of rows past nr had no reader
+        if (TF == 2)
+            lds_barrier();
+    }
+}
+
+template <int KIND> static auto i8_kernel(int BM)
+{
+    return BM == 32   ? i8_stream_kernel<KIND>
+           : BM == 64 ? i8_tile_kernel<KIND, 2>
+                      : i8_tile_kernel<KIND, 4>;
+}
+
+hipError_t launch_i8_gemm(int kind, const I8GemmArgs &a, int num_cus, hipStream_t s)
+{
+    const bool g1 = kind == I8_SWIGLU;
+    const int ntt = g1 ? a.NT : a.NT * a.panels;
+    const int per = a.BM == 32 ? (g1 ? 2 : 4) : (g1 ? 4 : 8);
+    const int64_t most = (int64_t)a.max_mtiles * ((ntt + per - 1) / per);
+    if (most >= ((int64_t)1 << 31))
+        return hipErrorInvalidValue;
+    if (most == 0)
+        return hipSuccess;
+    int64_t grid = (int64_t)num_cus * 2;
+    if (most < grid)
+        grid = most;
+    grid = (grid + 7) / 8 * 8; // a whole number of workgroups for each XCD
+    auto k = g1                ? i8_kernel<I8_SWIGLU>(a.BM)
+             : kind == I8_BF16 ? i8_kernel<I8_BF16>(a.BM)
+                               : i8_kernel<I8_F32>(a.BM);
+    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+} // namespace moe

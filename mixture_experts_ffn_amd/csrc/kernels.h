@@ -170,7 +170,8 @@ hipError_t launch_fast_fwd(int mode, int BM, const FastFwdArgs &a, int num_cus,
 hipError_t launch_fast_fwd_big(int mode, const FastFwdArgs &a, int num_cus, hipStream_t stream,
                                bool skip_padding = false);
 
-// bf16 engine (gemm_engine.hip): forward F1/F2 and backward B2/B4/B5/B7
+// bf16 engine (gemm_engine.hip): forward F1/F2, backward B2/B4/B5/B7 and the
+// grouped products' weight gradient GW
 struct EngineArgs {
     const bf16_t *A;             // first operand (see the kind table in gemm_engine.hip)
     const bf16_t *B;             // second operand
@@ -206,10 +207,10 @@ struct EngineArgs {
     // the backward set-up); null: an eighth of the tiles each
     const int32_t *xcd_bounds;
 };
-enum { ENG_F1 = 0, ENG_F2 = 1, ENG_B2 = 2, ENG_B4 = 3, ENG_B5 = 4, ENG_B7 = 5 };
+enum { ENG_F1 = 0, ENG_F2 = 1, ENG_B2 = 2, ENG_B4 = 3, ENG_B5 = 4, ENG_B7 = 5, ENG_GW = 6 };
 hipError_t launch_engine(int kind, int BM, const EngineArgs &a, int num_cus, hipStream_t stream);
 int engine_dgp_width(int I); // columns of the B2 partial-dot buffer
-// a weight-gradient kind's (ENG_B5 / ENG_B7) feature tiles per expert for an
+// a weight-gradient kind's (ENG_B5, ENG_B7, ENG_GW) feature tiles per expert for an
 // M x N gradient, and its workgroups per XCD
 void engine_feature_tiling(int kind, int M, int N, int num_cus, int *tiles_per_expert,
                            int *wg_per_xcd);
@@ -239,6 +240,75 @@ struct MxGemmArgs {
     int BM;                          // rows of an M-tile: 32, 64 or 128
 };
 hipError_t launch_mx_gemm(bool g1, int bits, const MxGemmArgs &a, int num_cus, hipStream_t s);
+
+// Bounds of a cost-balanced split of weight-gradient tiles over the XCDs.
+struct XcdSplits {
+    int n;          // launches (0..2)
+    int F[2];       // feature tiles per expert
+    int wgx[2];     // workgroups per XCD
+    int32_t *bounds; // [n][9]
+};
+
+// ---- row groups by offsets (group.hip) ---------------------------------------------
+// What the grouped products' kernels read, from a caller's offsets: checked
+// offsets, M-tile tables of BM rows (and of BM2, if not 0), the bounds of the
+// weight gradient's XCDs, zeroed tickets; and zeros in the rows of up to two
+// outputs that belong to no group.
+struct GroupSetup {
+    const void *offsets;          // [E + 1]; null: one group of all M rows
+    bool off64;
+    int64_t M;
+    int E, BM;
+    int32_t *out_offsets;         // [E + 1]
+    int32_t *mtile_off, *mtile_expert;
+    int32_t *tickets;             // [16]
+    XcdSplits splits;
+    void *out;                    // null: none
+    int64_t out_row;              // bytes of an output row, a multiple of 16
+};
+hipError_t launch_group_setup(const GroupSetup &g, hipStream_t s);
+
+// fp32 grouped products (gemm_f32.hip)
+struct F32Grouped {
+    const float *A, *B;           // NN: x, W [E, K, N]; NT: x, W [E, N, K]; TN: both by rows
+    float *C;
+    const int32_t *offsets, *mtile_off, *mtile_expert;
+    int E, M, N, K;               // TN: M x N of each gradient; else columns N, contraction K
+    int64_t lda, ldb;             // row strides
+    int max_mtiles;
+};
+enum { F32_NN = 0, F32_NT = 1, F32_TN = 2 };
+constexpr int kF32Rows = 64; // rows of an M-tile
+hipError_t launch_f32_grouped(int kind, const F32Grouped &a, hipStream_t s);
+
+// ---- int8 (layouts: i8.h) ---------------------------------------------------------
+hipError_t launch_i8_quantize_weight(int dtype, const void *w, void *codes, float *scales, int64_t E,
+                                     int64_t Kd, int64_t N, int panels, hipStream_t s);
+hipError_t launch_i8_pack_weight(const void *w, const float *w_scales, void *codes, float *scales,
+                                 int64_t E, int64_t Kd, int64_t N, int panels, hipStream_t s);
+hipError_t launch_i8_dequantize_weight(int dtype, const void *codes, const float *scales, void *w,
+                                       int64_t E, int64_t Kd, int64_t N, int panels, hipStream_t s);
+hipError_t launch_i8_quantize_rows(int dtype, const void *x, int64_t stride, void *codes,
+                                   float *scales, int64_t M, int64_t Kd, hipStream_t s);
+struct I8GemmArgs {
+    const uint8_t *wcodes;       // packed weights
+    const float *wscales;
+    const uint8_t *acodes;       // token rows, KS * 32 bytes each
+    const float *ascales;
+    void *out;                   // act [TK, N] fp32 (SwiGLU), else y [M, N]
+    const int32_t *sorted_slot;  // SwiGLU: permuted row -> slot
+    const int32_t *offsets, *mtile_off, *mtile_expert; // null tables: one group of M rows
+    int64_t M;                   // rows of acodes
+    int E, topk, N;              // N: output columns
+    int NT, KS;                  // column tiles of a panel, k-steps of 32
+    int panels;
+    int max_mtiles;              // upper bound of the M-tiles
+    int BM;                      // rows of an M-tile: 32, 64 or 128
+    bool stream_out;             // the output does not stay in the last-level cache
+};
+// kind: what the epilogue makes of the sums
+enum { I8_SWIGLU = 0, I8_BF16 = 1, I8_F32 = 2 };
+hipError_t launch_i8_gemm(int kind, const I8GemmArgs &a, int num_cus, hipStream_t s);
 
 // ---- router -----------------------------------------------------------------------
 struct RouterArgs {
@@ -290,12 +360,6 @@ hipError_t launch_zero_fill(void *p, size_t bytes, hipStream_t stream);
 // nine tile bounds of a cost-balanced split over the eight XCDs into
 // xcd_bounds[9 i .. 9 i + 8].
 enum { BWD_STAGE_ALL = 0, BWD_STAGE_D = 1, BWD_STAGE_W = 2 };
-struct XcdSplits {
-    int n;          // launches (0..2)
-    int F[2];       // feature tiles per expert
-    int wgx[2];     // workgroups per XCD
-    int32_t *bounds; // [n][9]
-};
 hipError_t launch_bwd_setup(const SavedHeader *hdr, uint64_t problem_hash, const int32_t *counts,
                             const int32_t *offsets, int E, int64_t TK, int BM, int32_t *counts_out,
                             int32_t *offsets_out, int32_t *mtile_off, int32_t *mtile_expert,
