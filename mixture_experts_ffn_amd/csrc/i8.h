@@ -29,44 +29,110 @@ struct I8Dims {
 
 __device__ inline uint32_t i8_abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// Scale and codes of a vector from the bits of its largest magnitude (as integers
-// they order as the values do, infinities and NaN above all numbers).
+// The largest magnitude of a vector's values, as the bits of an fp32 number (as
+// integers they order as the values do, infinities and NaN above all numbers).  bf16
+// values two at a time.
+template <typename T> struct I8Top;
+template <> struct I8Top<float> {
+    uint32_t t = 0;
+    __device__ void add(float v) { t = max(t, i8_abs_bits(v)); }
+    __device__ uint32_t bits() const { return t; }
+};
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+struct I8Top2 { // of either half of dwords
+    u16x2 t = {0, 0};
+    __device__ void add(uint32_t v)
+    {
+        t = __builtin_elementwise_max(t, __builtin_bit_cast(u16x2, v & 0x7fff7fffu));
+    }
+    __device__ uint32_t bits(int half) const { return (uint32_t)t[half] << 16; }
+    __device__ uint32_t bits() const { return max(bits(0), bits(1)); }
+};
+
+// Scale and codes of a vector with the largest magnitude `top`.
 struct I8Scale {
     float scale, inverse;
-    bool exact; // every quotient by division in 64 bits
+    float quick; // bf16: the factor of codes without a further look
+    bool exact;  // every quotient by division in 64 bits
+    bool ties;   // bf16: many quotients lie in the middle of two codes
 };
-__device__ inline I8Scale i8_scale(uint32_t top)
+template <typename T> __device__ inline I8Scale i8_scale(uint32_t top)
 {
-    I8Scale s;
-    if (top >= 0x7f800000u) { // NaN or infinity: the scale says it, the codes are 0
-        s.scale = __uint_as_float(0x7fc00000u);
-        s.inverse = 0.f;
-        s.exact = false;
+    I8Scale s{__uint_as_float(0x7fc00000u), 0.f, 0.f, false, false};
+    if (top >= 0x7f800000u) // NaN or infinity: the scale says it, the codes are 0
         return s;
-    }
-    s.scale = (float)((double)__uint_as_float(top) / 127.0);
+    const float largest = __uint_as_float(top);
+    s.scale = largest / 127.0f;
+    if (s.scale == 0.f)
+        return s;
     // the reciprocal of a scale below 2^-126 overflows or has lost bits, of one near
     // 2^126 is subnormal
     s.exact = s.scale < 0x1p-100f || s.scale > 0x1p100f;
-    s.inverse = s.scale > 0.f ? 1.0f / s.scale : 0.f;
-    if (s.scale == 0.f)
-        s.exact = false;
+    s.inverse = 1.0f / s.scale;
+    if constexpr (sizeof(T) == 2) {
+        // v and largest have 8 bits: 254 v / largest is an odd integer (or within
+        // 2^-23 of one, scale being rounded) only for v = largest / 2, whose side of
+        // 63.5 the factor is moved to, and, among others, where largest is 127 times a
+        // power of two; else it is 1 / 255 away, so that 2^-20 of error do no harm
+        const float rest = fmaf(-63.5f, s.scale, 0.5f * largest); // exact (see i8_codes)
+        s.quick = s.inverse * (rest >= 0.f ? 1.f + 0x1p-21f : 1.f - 0x1p-21f);
+        s.ties = (top >> 16 & 0x7fu) == 0x7eu;
+    }
     return s;
 }
 
-// The code of v.  v * inverse is within 2^-23 of v / scale, relatively (the
-// reciprocal's and the product's rounding), 1.6e-5 at 127: a quotient that lies
-// within 4e-5 of the middle of two codes is formed again in 64 bits, where a middle
-// is told from its neighbours (v and scale are fp32, so that a quotient beside a
-// middle is 2^-32 away at least).
-__device__ inline int i8_code(float v, const I8Scale &s)
+// Codes of N values (a multiple of 4), packed four to a dword, of a vector of T.  Each is
+// made as code + 128 in its byte (rounded to nearest even by the conversion).
+//
+// t = v * inverse is within 2^-23 of v / scale, relatively (the reciprocal's and the
+// product's rounding), so it never rounds past 127.  Where some quotient may lie on the
+// other side of the middle of two codes than t, or on it, all N are compared with it
+// by their rest e = v - code * scale, one multiply-add: where it decides, e is a
+// multiple of half a unit in scale's last place, below 2^24 of them, so exact.  Of a
+// vector with a NaN or an infinity (or of zeros) all codes are 0.
+template <typename T, int N>
+__device__ inline void i8_codes(const float *v, const I8Scale &s, uint32_t *out)
 {
-    float t = v * s.inverse;
-    float r = rintf(t);
-    if (s.exact || fabsf(t - r) > 0.49996f)
-        r = s.inverse == 0.f ? 0.f : (float)rint((double)v / (double)s.scale);
-    // a NaN or an infinity among v: codes 0
-    return s.inverse == 0.f ? 0 : (int)fminf(fmaxf(r, -127.f), 127.f);
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            uint32_t u = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                u = __builtin_amdgcn_cvt_pk_u8_f32(fmaf(v[4 * i + b], s.quick, 128.f), b, u);
+            out[i] = s.quick == 0.f ? 0u : u ^ 0x80808080u;
+        }
+        if (!(s.exact || s.ties))
+            return;
+    }
+    float r[N], near = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float t = v[i] * s.inverse;
+        r[i] = rintf(t);
+        near = fmaxf(near, fabsf(t - r[i]));
+    }
+    if (s.exact) {
+#pragma unroll 1
+        for (int i = 0; i < N; ++i)
+            r[i] = fminf(fmaxf((float)rint((double)v[i] / (double)s.scale), -127.f), 127.f);
+    } else if (near > 0.49998f) { // 127 * 2^-23 is 1.6e-5
+        const float half = 0.5f * s.scale;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float e = fmaf(-r[i], s.scale, v[i]), a = fabsf(e);
+            if (a > half || (a == half && ((int)r[i] & 1)))
+                r[i] += copysignf(1.f, e);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+        uint32_t u = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+            u = __builtin_amdgcn_cvt_pk_u8_f32(r[4 * i + b] + 128.f, b, u);
+        out[i] = s.inverse == 0.f ? 0u : u ^ 0x80808080u;
+    }
 }
 
 __device__ inline uint32_t i8_pack4(int a, int b, int c, int d)
