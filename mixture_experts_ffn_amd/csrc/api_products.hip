@@ -150,7 +150,7 @@ hipError_t run_rows(int dtype, const RowsProduct &p, const RowsPlan &plan, int64
         a.lda = p.lda;
         a.ldb = p.nt ? p.K : p.N;
         a.max_mtiles = (int)moe::max_mtiles_bound(p.M, (int)E, moe::kF32Rows);
-        return moe::launch_f32_grouped(p.nt ? moe::F32_NT : moe::F32_NN, a, s);
+        return moe::launch_f32_grouped(p.nt ? moe::F32_NT : moe::F32_NN, a, num_cus, s);
     }
     if (plan.fast) {
         moe::FastFwdArgs a{};
@@ -301,7 +301,7 @@ int moe_ffn_grouped_mm_bwd(const moe_ffn_grouped *g, const void *dy, const void 
         w.N = wn;
         w.lda = lda;
         w.ldb = ldb;
-        HIP_TRY(moe::launch_f32_grouped(moe::F32_TN, w, s), "weight gradient launch");
+        HIP_TRY(moe::launch_f32_grouped(moe::F32_TN, w, num_cus, s), "weight gradient launch");
         return MOE_FFN_OK;
     }
     moe::EngineArgs w{};

@@ -5,71 +5,80 @@
 //   TN  dW[e] = sum_{m in e} a[m]^T b[m]
 //
 // Tiles of 64 x 64 outputs, 32 deep, four waves of 32 x 32, on the fp32 matrix
-// instruction (16 x 16 x 4, products and sums in fp32).  Both operands lie in LDS
-// with k outermost, so that a fragment is 16 consecutive values of four k rows,
-// which a row length of 80 spreads over all banks; an operand that is contiguous
-// along k is turned on the way in.  Two buffers, the next step's loads under the
-// current one's products.  Bound by the matrix instruction: 256 flops a clock and
-// CU, 32 clocks each, of which the four fragment reads of a step hide behind four.
+// instruction (16 x 16 x 4, products and sums in fp32); where these are too few for
+// the CUs, tiles of 32 x 32 whose waves take a quarter of each step's k and are summed
+// through LDS.  Both operands lie in LDS with k outermost, so that a fragment is 16
+// consecutive values of four k rows; an operand that is contiguous along k is turned
+// on the way in.  Two LDS buffers, and the loads of the next two steps in registers,
+// since a step of a lone workgroup is shorter than a load.  Bound by the matrix
+// instruction (256 flops a clock and CU) in large problems, by the length of the chain
+// of steps in small ones.
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 
 namespace moe {
 namespace f32 {
 
-constexpr int BT = 64, BK = 32, LD = BT + 16;
+constexpr int BK = 32;
 
-// A 64 x 32 operand tile on its way from memory to LDS: two 16-byte pieces a thread.
-// KC: the operand is contiguous along k (piece: 4 k of a row), else along its
-// rows (piece: 4 rows of a k).  What lies outside is zero.
-template <bool KC> struct Stage {
-    const float *p[2];
-    bool ok[2];
-    int r[2], k[2];
-    f32x4 v[2];
+// A BT x 32 operand tile on its way from memory to LDS, 16-byte pieces.  KC: the
+// operand is contiguous along k (piece: 4 k of a row), else along its rows (piece: 4
+// rows of a k).  What lies outside is zero.
+template <bool KC, int BT> struct Stage {
+    static constexpr int LD = BT + 20; // the turned pieces' rows fall in different banks
+    static constexpr int NP = BT * BK / 4 / 256, RP = BT / 4;
+    const float *p[NP];
+    bool ok[NP];
+    int r[NP], k[NP];
+    f32x4 v[2][NP];
 
     __device__ void place(const float *base, int64_t ld, int valid_r)
     {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NP; ++i) {
             const int u = threadIdx.x + i * 256;
-            r[i] = KC ? u >> 3 : (u & 15) * 4;
-            k[i] = KC ? (u & 7) * 4 : u >> 4;
+            r[i] = KC ? u / (BK / 4) : u % RP * 4;
+            k[i] = KC ? u % (BK / 4) * 4 : u / RP;
             ok[i] = r[i] < valid_r; // a multiple of 4 rows where pieces run along them
             p[i] = base + (ok[i] ? KC ? r[i] * ld + k[i] : k[i] * ld + r[i] : 0);
         }
     }
-    __device__ void load(int64_t ld, int k0, int K)
+    __device__ void load(int slot, int64_t ld, int k0, int K)
     {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) // along k: K is a multiple of 8
-            v[i] = ok[i] && k0 + k[i] < K
-                       ? *reinterpret_cast<const f32x4 *>(p[i] + (KC ? k0 : k0 * ld))
-                       : f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < NP; ++i) // along k: K is a multiple of 8
+            v[slot][i] = ok[i] && k0 + k[i] < K
+                             ? *reinterpret_cast<const f32x4 *>(p[i] + (KC ? k0 : k0 * ld))
+                             : f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    __device__ void store(float *s) const
+    __device__ void store(int slot, float *s) const
     {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NP; ++i) {
             if constexpr (KC) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    s[(k[i] + j) * LD + r[i]] = v[i][j];
+                    s[(k[i] + j) * LD + r[i]] = v[slot][i][j];
             } else {
-                *reinterpret_cast<f32x4 *>(s + k[i] * LD + r[i]) = v[i];
+                *reinterpret_cast<f32x4 *>(s + k[i] * LD + r[i]) = v[slot][i];
             }
         }
     }
 };
 
-template <int KIND> __global__ __launch_bounds__(256) void f32_grouped_kernel(F32Grouped a)
+template <int KIND, int BT> __global__ __launch_bounds__(256) void f32_grouped_kernel(F32Grouped a)
 {
     constexpr bool TN = KIND == F32_TN;
+    constexpr int LD = BT + 20, MT = kF32Rows / BT; // tiles of an M-tile's rows
     __shared__ __attribute__((aligned(16))) float sA[2][BK * LD], sB[2][BK * LD];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
+    const int wm = BT == 64 ? (wave >> 1) * 32 : 0, wn = BT == 64 ? (wave & 1) * 32 : 0;
+    const int wk = BT == 64 ? 0 : wave * 8; // 32: this wave's part of a step
+    constexpr int KW = BT == 64 ? BK : 8;
     const int ntm = TN ? (a.M + BT - 1) / BT : 0, ntn = (a.N + BT - 1) / BT;
-    const int64_t total = TN ? (int64_t)a.E * ntm * ntn : (int64_t)a.mtile_off[a.E] * ntn;
+    const int64_t total = TN ? (int64_t)a.E * ntm * ntn : (int64_t)a.mtile_off[a.E] * MT * ntn;
     for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
         // group-major; inside a group column tiles outer, so that tiles in flight share weights
         int e, r0, rows, K;
@@ -84,18 +93,20 @@ template <int KIND> __global__ __launch_bounds__(256) void f32_grouped_kernel(F3
             first = a.offsets[e];
             K = a.offsets[e + 1] - (int)first;
         } else {
-            e = a.mtile_expert[t / ntn];
-            const int mt0 = a.mtile_off[e], mts = a.mtile_off[e + 1] - mt0;
+            e = a.mtile_expert[t / (MT * ntn)];
+            const int mt0 = a.mtile_off[e] * MT, mts = a.mtile_off[e + 1] * MT - mt0;
             const int64_t local = t - (int64_t)mt0 * ntn;
             n0 = (int)(local / mts) * BT;
             r0 = a.offsets[e] + (int)(local % mts) * BT;
             rows = min(BT, a.offsets[e + 1] - r0);
             first = r0;
             K = a.K;
+            if (rows <= 0) // the second half of a group's last M-tile
+                continue;
         }
         const int cols = min(BT, a.N - n0);
-        Stage<!TN> A;
-        Stage<KIND == F32_NT> B;
+        Stage<!TN, BT> A;
+        Stage<KIND == F32_NT, BT> B;
         A.place(TN ? a.A + first * a.lda + r0 : a.A + first * a.lda, a.lda, rows);
         if constexpr (TN)
             B.place(a.B + first * a.ldb + n0, a.ldb, cols);
@@ -109,21 +120,23 @@ template <int KIND> __global__ __launch_bounds__(256) void f32_grouped_kernel(F3
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-        A.load(a.lda, 0, K);
-        B.load(a.ldb, 0, K);
         const int nk = (K + BK - 1) / BK;
-        for (int s = 0; s < nk; ++s) {
-            A.store(sA[s & 1]);
-            B.store(sB[s & 1]);
-            __syncthreads();
-            if (s + 1 < nk) {
-                A.load(a.lda, (s + 1) * BK, K);
-                B.load(a.ldb, (s + 1) * BK, K);
-            }
-            const float *pa = sA[s & 1] + (lane >> 4) * LD + (lane & 15) + wm;
-            const float *pb = sB[s & 1] + (lane >> 4) * LD + (lane & 15) + wn;
 #pragma unroll
-            for (int k = 0; k < BK; k += 4) {
+        for (int s = 0; s < 2; ++s) {
+            A.load(s, a.lda, s * BK, K);
+            B.load(s, a.ldb, s * BK, K);
+        }
+        auto step = [&](int s, auto SLOT) {
+            constexpr int slot = decltype(SLOT)::value; // of registers and of LDS
+            A.store(slot, sA[slot]);
+            B.store(slot, sB[slot]);
+            __syncthreads();
+            A.load(slot, a.lda, (s + 2) * BK, K);
+            B.load(slot, a.ldb, (s + 2) * BK, K);
+            const float *pa = sA[slot] + (wk + (lane >> 4)) * LD + (lane & 15) + wm;
+            const float *pb = sB[slot] + (wk + (lane >> 4)) * LD + (lane & 15) + wn;
+#pragma unroll
+            for (int k = 0; k < KW; k += 4) {
                 const float a0 = pa[k * LD], a1 = pa[k * LD + 16];
                 const float b0 = pb[k * LD], b1 = pb[k * LD + 16];
                 // the columns as the instruction's rows: a lane then holds four
@@ -133,37 +146,62 @@ template <int KIND> __global__ __launch_bounds__(256) void f32_grouped_kernel(F3
                 acc[1][0] = Mfma<float>::mma(b0, a1, acc[1][0]);
                 acc[1][1] = Mfma<float>::mma(b1, a1, acc[1][1]);
             }
-        }
+        };
         // the buffer of step s is written again in step s + 2, after the barrier of s + 1
-        float *C = TN ? a.C + (int64_t)e * a.M * a.N : a.C;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = wm + 16 * i + (lane & 15);
-            if (r < rows)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int c = wn + 16 * j + (lane >> 4) * 4;
-                    if (c < cols) // cols is a multiple of 8
-                        *reinterpret_cast<f32x4 *>(C + (int64_t)(r0 + r) * a.N + n0 + c) = acc[i][j];
-                }
+        for (int s = 0; s < nk; s += 2) {
+            step(s, std::integral_constant<int, 0>{});
+            if (s + 1 < nk)
+                step(s + 1, std::integral_constant<int, 1>{});
         }
-        __syncthreads(); // the next tile writes the buffers from the first on
+        float *C = TN ? a.C + (int64_t)e * a.M * a.N : a.C;
+        auto out = [&](int i, int j, f32x4 v) {
+            const int r = wm + 16 * i + (lane & 15), c = wn + 16 * j + (lane >> 4) * 4;
+            if (r < rows && c < cols) // cols is a multiple of 8
+                *reinterpret_cast<f32x4 *>(C + (int64_t)(r0 + r) * a.N + n0 + c) = v;
+        };
+        __syncthreads(); // every wave is past its reads: the buffers may be written
+        if constexpr (BT == 64) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    out(i, j, acc[i][j]);
+        } else {
+            // wave w sums block w, in the order of the waves
+            f32x4 *red = reinterpret_cast<f32x4 *>(wave < 2 ? sA[0] : sB[0]) + (wave & 1) * 256;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                red[b * 64 + lane] = acc[b >> 1][b & 1];
+            __syncthreads();
+            f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                v += (reinterpret_cast<const f32x4 *>(w < 2 ? sA[0] : sB[0]) + (w & 1) * 256)[wave * 64 + lane];
+            out(wave >> 1, wave & 1, v);
+            __syncthreads();
+        }
     }
 }
 
 } // namespace f32
 
-hipError_t launch_f32_grouped(int kind, const F32Grouped &a, hipStream_t s)
+// Tiles of 32 x 32 while there are fewer than two of 64 x 64 for each CU.
+hipError_t launch_f32_grouped(int kind, const F32Grouped &a, int num_cus, hipStream_t s)
 {
-    const int64_t ntn = (a.N + f32::BT - 1) / f32::BT;
-    const int64_t tiles =
-        kind == F32_TN ? (int64_t)a.E * ((a.M + f32::BT - 1) / f32::BT) * ntn : a.max_mtiles * ntn;
-    if (tiles <= 0)
+    auto tiles = [&](int bt) {
+        const int64_t ntn = (a.N + bt - 1) / bt;
+        return kind == F32_TN ? (int64_t)a.E * ((a.M + bt - 1) / bt) * ntn
+                              : (int64_t)a.max_mtiles * (kF32Rows / bt) * ntn;
+    };
+    const bool small = tiles(64) < 2 * (int64_t)num_cus;
+    const int64_t n = tiles(small ? 32 : 64);
+    if (n <= 0)
         return hipSuccess;
-    const dim3 grid((unsigned)(tiles < 65536 ? tiles : 65536));
-    auto k = kind == F32_NN   ? f32::f32_grouped_kernel<F32_NN>
-             : kind == F32_NT ? f32::f32_grouped_kernel<F32_NT>
-                              : f32::f32_grouped_kernel<F32_TN>;
+    const dim3 grid((unsigned)(n < 65536 ? n : 65536));
+    auto k = kind == F32_NN   ? small ? f32::f32_grouped_kernel<F32_NN, 32> : f32::f32_grouped_kernel<F32_NN, 64>
+             : kind == F32_NT ? small ? f32::f32_grouped_kernel<F32_NT, 32> : f32::f32_grouped_kernel<F32_NT, 64>
+             : small          ? f32::f32_grouped_kernel<F32_TN, 32>
+                              : f32::f32_grouped_kernel<F32_TN, 64>;
     hipLaunchKernelGGL(k, grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }

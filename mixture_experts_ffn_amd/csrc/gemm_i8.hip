@@ -97,25 +97,26 @@ __device__ inline I8Columns i8_columns(const I8GemmArgs &a, int tile)
     return {panel * pc + (tile - panel * a.NT) * 32, (panel + 1) * pc};
 }
 
-// Weight streaming kernel.  A tile is 32 token rows of one group times four column
-// tiles (SwiGLU: two gate and the same two up tiles); the four waves split the
+// Weight streaming kernel.  A tile is 32 token rows of one group times CT column
+// tiles (SwiGLU: half gate and the same up tiles); the WV waves split the
 // contraction, each streaming its part of the weights from memory straight into
-// registers, and are summed through LDS at the end.  What a wave needs is in
-// flight two k-step pairs (16 KB of weights) ahead, across the end of a tile too.
-struct I8Pair2 {
-    u32x4 w[4][2]; // [tile][k-step]
+// registers with the next D - 1 pairs of k-steps in flight, across the end of a tile
+// too, and are summed through LDS at the end.
+template <int CT> struct I8Part {
+    u32x4 w[CT][2]; // [tile][k-step]
     u32x4 a[2];
 };
 
-template <int KIND> __global__ __launch_bounds__(256, 2) void i8_stream_kernel(I8GemmArgs a)
+template <int KIND, int CT, int WV, int D>
+__global__ __launch_bounds__(64 * WV, 8 / WV > 1 ? 8 / WV : 1) void i8_stream_kernel(I8GemmArgs a)
 {
     using namespace tile;
     constexpr bool G1 = KIND == I8_SWIGLU;
-    __shared__ i32x4 red[4][3][4][64]; // [tile][other wave][register / 4][lane]
+    __shared__ i32x4 red[WV][CT][4][64]; // [wave][tile][register / 4][lane]
     const int lane = threadIdx.x & 63;
     const int wave = uni(threadIdx.x >> 6);
     const int h = lane >> 5;
-    constexpr int PER = G1 ? 2 : 4; // column tiles of a panel
+    constexpr int PER = G1 ? CT / 2 : CT; // column tiles of a panel
     const int ntt = G1 ? a.NT : a.NT * a.panels;
     const int ncg = (ntt + PER - 1) / PER;
     const int64_t total = (int64_t)i8_mtiles(a) * ncg;
@@ -125,16 +126,19 @@ template <int KIND> __global__ __launch_bounds__(256, 2) void i8_stream_kernel(I
     const int64_t t1 = total * (xcd + 1) / 8;
     // the wave's k-step pairs [p0, p1)
     const int KP = a.KS >> 1;
-    const int p0 = KP * wave / 4, p1 = KP * (wave + 1) / 4;
+    const int p0 = KP * wave / WV, p1 = KP * (wave + 1) / WV;
 
     struct Place {
         int e, cg, nr, row;
         uint32_t ao;                    // this lane's token row
         float as;                       // and its scale
         __amdgpu_buffer_rsrc_t ac, wc;  // token rows, the group's weights
-        int tile[4];                    // column tiles, counted from there
+        int tile[CT];                   // column tiles, counted from there
     };
     const int64_t etiles = (int64_t)a.NT * a.panels; // of a group's weights
+    auto column_tile = [&](int cg, int j) { // SwiGLU: gate tiles, then their up tiles
+        return min(cg * PER + j % PER, ntt - 1) + (G1 ? j / PER * a.NT : 0);
+    };
     auto place = [&](int64_t t, Place &q) {
         const int m = (int)(t / ncg);
         q.cg = uni((int)(t - (int64_t)m * ncg));
@@ -151,130 +155,93 @@ template <int KIND> __global__ __launch_bounds__(256, 2) void i8_stream_kernel(I
         q.ao = (uint32_t)(arow - first) * (uint32_t)(a.KS * 32) + h * 16;
         q.wc = i8_bytes(a.wcodes + g.e * etiles * a.KS * 1024, (uint32_t)(etiles * a.KS * 1024));
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            q.tile[j] = min(q.cg * PER + (G1 ? j >> 1 : j), ntt - 1) + (G1 ? (j & 1) * a.NT : 0);
+        for (int j = 0; j < CT; ++j)
+            q.tile[j] = column_tile(q.cg, j);
     };
     const uint32_t wl = lane * 16;
-    auto load = [&](const Place &q, int p, I8Pair2 &x) {
+    auto load = [&](const Place &q, int p, I8Part<CT> &x) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             x.a[s] = __builtin_amdgcn_raw_buffer_load_b128(q.ac, q.ao + s * 32, p * 64, 0);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < CT; ++j)
                 x.w[j][s] = __builtin_amdgcn_raw_buffer_load_b128(
                     q.wc, wl + s * 1024, i8_code_offset(q.tile[j], a.KS, p * 2), kOnce);
         }
     };
-    i32x16 acc[4];
-    auto compute = [&](const I8Pair2 &x) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[j] = i8_mma(x.w[j][s], x.a[s], acc[j]);
-    };
-
     int64_t t = total * xcd / 8 + (blockIdx.x >> 3);
     if (t >= t1)
         return;
     Place q;
-    I8Pair2 x, y;
+    I8Part<CT> x[D];
     auto first = [&] {
         place(t, q);
-        if (p0 < p1)
-            load(q, p0, x);
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            if (p0 + d < p1)
+                load(q, p0 + d, x[d]);
     };
     first();
     while (true) {
+        i32x16 acc[CT];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < CT; ++j)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 acc[j][i] = 0;
-        for (int p = p0; p < p1; p += 2) {
-            if (p + 1 < p1)
-                load(q, p + 1, y);
-            compute(x);
-            if (p + 1 < p1) {
-                if (p + 2 < p1)
-                    load(q, p + 2, x);
-                compute(y);
-            }
-        }
+        for (int p = p0; p < p1; p += D)
+#pragma unroll
+            for (int d = 0; d < D; ++d)
+                if (p + d < p1) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int j = 0; j < CT; ++j)
+                            acc[j] = i8_mma(x[d].w[j][s], x[d].a[s], acc[j]);
+                    if (p + d + D < p1)
+                        load(q, p + d + D, x[d]);
+                }
         const int cg = q.cg, nr = q.nr, row = q.row, e = q.e;
         const float as = q.as;
         t += gridDim.x >> 3;
         if (t < t1)
             first();
-        // wave w sums tile w
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j != wave) {
-                const int slot = wave < j ? wave : wave - 1;
+        for (int j = 0; j < CT; ++j)
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    red[j][slot][q][lane] =
-                        i32x4{acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]};
-            }
+            for (int r = 0; r < 4; ++r)
+                red[wave][j][r][lane] =
+                    i32x4{acc[j][4 * r], acc[j][4 * r + 1], acc[j][4 * r + 2], acc[j][4 * r + 3]};
         __syncthreads();
-        i32x16 sum;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j == wave)
-                sum = acc[j];
-#pragma unroll
-        for (int s = 0; s < 3; ++s)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const i32x4 v = red[wave][s][q][lane];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sum[4 * q + i] += v[i];
-            }
         const bool live = (lane & 31) < nr;
-        // this wave's column tile
-        const int ct = min(cg * PER + (G1 ? wave >> 1 : wave), ntt - 1) + (G1 ? (wave & 1) * a.NT : 0);
-        const float *cs = a.wscales + (e * etiles + ct) * 32 + 4 * h;
-        f32x4 out[4];
+        // four columns of a token: tile j, register group r
+        auto sum = [&](int j, int r) {
+            i32x4 v = red[0][j][r][lane];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            out[q] = i8_scaled(sum, q, as, *reinterpret_cast<const f32x4 *>(cs + 8 * q));
-        if constexpr (G1) {
-            __syncthreads();
-            if (wave & 1) { // the up tile goes to the wave of its gate tile
+            for (int w = 1; w < WV; ++w)
+                v += red[w][j][r][lane];
+            const f32x4 cs = *reinterpret_cast<const f32x4 *>(
+                a.wscales + (e * etiles + column_tile(cg, j)) * 32 + 8 * r + 4 * h);
+            f32x4 o;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    red[wave][0][q][lane] = __builtin_bit_cast(i32x4, out[q]);
-            }
-            __syncthreads();
-            if (!(wave & 1)) {
-                const int c = cg * 2 + (wave >> 1);
-                float *orow = static_cast<float *>(a.out) + (int64_t)row * a.N;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const f32x4 up = __builtin_bit_cast(f32x4, red[wave + 1][0][q][lane]);
-                    const int col = c * 32 + 8 * q + 4 * h;
-                    if (live && c < a.NT && col < a.N)
-                        *reinterpret_cast<f32x4 *>(orow + col) = i8_swiglu(out[q], up);
-                }
-            }
-        } else {
-            const I8Columns cols = i8_columns(a, ct);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int col = cols.first + 8 * q + 4 * h;
-                if (live && cg * PER + wave < ntt && col < cols.end) {
-                    if constexpr (KIND == I8_F32) {
-                        *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + (int64_t)row * a.N +
-                                                   col) = out[q];
-                    } else {
-                        const bf16x4 o = {(bf16)out[q][0], (bf16)out[q][1], (bf16)out[q][2],
-                                          (bf16)out[q][3]};
-                        *reinterpret_cast<bf16x4 *>(static_cast<bf16 *>(a.out) + (int64_t)row * a.N +
-                                                    col) = o;
-                    }
-                }
-            }
+            for (int i = 0; i < 4; ++i)
+                o[i] = (float)v[i] * as * cs[i];
+            return o;
+        };
+        for (int it = wave; it < PER * 4; it += WV) {
+            const int j = it >> 2, r = it & 3;
+            const f32x4 o = G1 ? i8_swiglu(sum(j, r), sum(j + PER, r)) : sum(j, r);
+            const I8Columns cols = G1 ? I8Columns{(cg * PER + j) * 32, a.N}
+                                      : i8_columns(a, column_tile(cg, j));
+            const int col = cols.first + 8 * r + 4 * h;
+            if (!live || cg * PER + j >= ntt || col >= cols.end)
+                continue;
+            const int64_t at = (int64_t)row * a.N + col;
+            if constexpr (KIND == I8_BF16)
+                *reinterpret_cast<bf16x4 *>(static_cast<bf16 *>(a.out) + at) =
+                    bf16x4{(bf16)o[0], (bf16)o[1], (bf16)o[2], (bf16)o[3]};
+            else
+                *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at) = o;
         }
         if (t >= t1)
             return;
@@ -517,31 +484,46 @@ __global__ __launch_bounds__(256, 2) void i8_tile_kernel(I8GemmArgs a)
     }
 }
 
-template <int KIND> static auto i8_kernel(int BM)
+template <int KIND>
+static void i8_launch(const I8GemmArgs &a, int num_cus, hipStream_t s)
 {
-    return BM == 32   ? i8_stream_kernel<KIND>
-           : BM == 64 ? i8_tile_kernel<KIND, 2>
-                      : i8_tile_kernel<KIND, 4>;
+    constexpr bool G1 = KIND == I8_SWIGLU;
+    const int ntt = G1 ? a.NT : a.NT * a.panels;
+    auto run = [&](auto *kernel, int per, int threads, int groups_a_cu) {
+        const int64_t most = (int64_t)a.max_mtiles * ((ntt + per - 1) / per);
+        int64_t grid = (int64_t)num_cus * groups_a_cu;
+        if (most < grid)
+            grid = most;
+        grid = (grid + 7) / 8 * 8; // a whole number of workgroups for each XCD
+        hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3((unsigned)threads), 0, s, a);
+    };
+    if (a.BM == 32) {
+        // tiles of two column tiles by four waves, if there is one for each CU; else a
+        // single one (SwiGLU: a pair) by eight
+        if ((int64_t)a.max_mtiles * (G1 ? ntt : (ntt + 1) / 2) >= num_cus)
+            run(i8_stream_kernel<KIND, 2, 4, 4>, G1 ? 1 : 2, 256, 2);
+        else
+            run(i8_stream_kernel<KIND, G1 ? 2 : 1, 8, 4>, 1, 512, 2);
+    } else if (a.BM == 64) {
+        run(i8_tile_kernel<KIND, 2>, G1 ? 4 : 8, 256, 2);
+    } else {
+        run(i8_tile_kernel<KIND, 4>, G1 ? 4 : 8, 256, 2);
+    }
 }
 
 hipError_t launch_i8_gemm(int kind, const I8GemmArgs &a, int num_cus, hipStream_t s)
 {
-    const bool g1 = kind == I8_SWIGLU;
-    const int ntt = g1 ? a.NT : a.NT * a.panels;
-    const int per = a.BM == 32 ? (g1 ? 2 : 4) : (g1 ? 4 : 8);
-    const int64_t most = (int64_t)a.max_mtiles * ((ntt + per - 1) / per);
-    if (most >= ((int64_t)1 << 31))
+    const int64_t columns = (int64_t)a.NT * a.panels;
+    if (a.max_mtiles * columns >= ((int64_t)1 << 31))
         return hipErrorInvalidValue;
-    if (most == 0)
+    if (a.max_mtiles == 0)
         return hipSuccess;
-    int64_t grid = (int64_t)num_cus * 2;
-    if (most < grid)
-        grid = most;
-    grid = (grid + 7) / 8 * 8; // a whole number of workgroups for each XCD
-    auto k = g1                ? i8_kernel<I8_SWIGLU>(a.BM)
-             : kind == I8_BF16 ? i8_kernel<I8_BF16>(a.BM)
-                               : i8_kernel<I8_F32>(a.BM);
-    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(256), 0, s, a);
+    if (kind == I8_SWIGLU)
+        i8_launch<I8_SWIGLU>(a, num_cus, s);
+    else if (kind == I8_BF16)
+        i8_launch<I8_BF16>(a, num_cus, s);
+    else
+        i8_launch<I8_F32>(a, num_cus, s);
     return hipGetLastError();
 }
 

@@ -279,7 +279,7 @@ struct F32Grouped {
 };
 enum { F32_NN = 0, F32_NT = 1, F32_TN = 2 };
 constexpr int kF32Rows = 64; // rows of an M-tile
-hipError_t launch_f32_grouped(int kind, const F32Grouped &a, hipStream_t s);
+hipError_t launch_f32_grouped(int kind, const F32Grouped &a, int num_cus, hipStream_t s);
 
 // ---- int8 (layouts: i8.h) ---------------------------------------------------------
 hipError_t launch_i8_quantize_weight(int dtype, const void *w, void *codes, float *scales, int64_t E,
