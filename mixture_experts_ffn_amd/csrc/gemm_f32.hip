@@ -135,17 +135,33 @@ template <int KIND, int BT> __global__ __launch_bounds__(256) void f32_grouped_k
             B.load(slot, a.ldb, (s + 2) * BK, K);
             const float *pa = sA[slot] + (wk + (lane >> 4)) * LD + (lane & 15) + wm;
             const float *pb = sB[slot] + (wk + (lane >> 4)) * LD + (lane & 15) + wn;
+            constexpr int NK = KW / 4;
+            float fa[NK][2], fb[NK][2];
 #pragma unroll
-            for (int k = 0; k < KW; k += 4) {
-                const float a0 = pa[k * LD], a1 = pa[k * LD + 16];
-                const float b0 = pb[k * LD], b1 = pb[k * LD + 16];
-                // the columns as the instruction's rows: a lane then holds four
-                // neighbouring columns of one row
-                acc[0][0] = Mfma<float>::mma(b0, a0, acc[0][0]);
-                acc[0][1] = Mfma<float>::mma(b1, a0, acc[0][1]);
-                acc[1][0] = Mfma<float>::mma(b0, a1, acc[1][0]);
-                acc[1][1] = Mfma<float>::mma(b1, a1, acc[1][1]);
+            for (int k = 0; k < NK; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    fa[k][i] = pa[4 * k * LD + 16 * i];
+                    fb[k][i] = pb[4 * k * LD + 16 * i];
+                }
+            // the columns as the instruction's rows: a lane then holds four
+            // neighbouring columns of one row
+#pragma unroll
+            for (int k = 0; k < NK; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[i][j] = Mfma<float>::mma(fb[k][j], fa[k][i], acc[i][j]);
+            // the fragments of two k ahead of the products that take them
+            constexpr int AHEAD = NK < 2 ? NK : 2;
+            __builtin_amdgcn_sched_group_barrier(0x100, 2 * AHEAD, 0);
+#pragma unroll
+            for (int k = 0; k < NK - AHEAD; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
             }
+            __builtin_amdgcn_sched_group_barrier(0x008, 4 * AHEAD, 0);
         };
         // the buffer of step s is written again in step s + 2, after the barrier of s + 1
         for (int s = 0; s < nk; s += 2) {
