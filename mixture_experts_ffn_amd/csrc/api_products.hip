@@ -27,7 +27,7 @@ struct Taker {
 
 // What the grouped kernels walk, in a workspace (group.hip).
 struct GroupLayout {
-    size_t offsets, mtile_off, mtile_expert, tickets, xcd_bounds;
+    size_t offsets, mtile_off, mtile_expert, tickets, order;
     int64_t max_mtiles;
     void lay(Taker &take, int64_t M, int64_t E, int min_rows)
     {
@@ -36,7 +36,7 @@ struct GroupLayout {
         mtile_off = take(sizeof(int32_t) * (size_t)(E + 1));
         mtile_expert = take(sizeof(int32_t) * (size_t)max_mtiles);
         tickets = take(sizeof(int32_t) * 16);
-        xcd_bounds = take(sizeof(int32_t) * 9);
+        order = take(sizeof(int32_t) * (size_t)E);
     }
     moe::GroupSetup setup(void *ws, const void *given, int offsets_dtype, int64_t M, int64_t E, int BM) const
     {
@@ -50,7 +50,6 @@ struct GroupLayout {
         g.mtile_off = at<int32_t>(ws, mtile_off);
         g.mtile_expert = at<int32_t>(ws, mtile_expert);
         g.tickets = at<int32_t>(ws, tickets);
-        g.splits.bounds = at<int32_t>(ws, xcd_bounds);
         return g;
     }
 };
@@ -125,8 +124,9 @@ RowsPlan plan_rows(int dtype, const RowsProduct &p, int64_t E)
     if (dtype == MOE_FFN_F32)
         return r; // moe::kF32Rows
     const double rows = (double)p.M / (double)E;
-    r.fast = !p.nt && p.lda == p.K && moe::fast_gemm_supported(1, p.N, p.K);
-    r.big = r.fast && rows > 256 && p.M * p.K * 2 < (int64_t(1) << 32); // 32-bit row offsets
+    r.big = rows > 256 && p.K % 32 == 0 && p.K >= 128 &&
+            p.M * p.lda * 2 < (int64_t(1) << 32); // 32-bit row offsets
+    r.fast = !r.big && !p.nt && p.lda == p.K && moe::fast_gemm_supported(1, p.N, p.K);
     r.BM = r.big ? 256 : rows <= 64 ? 64 : 128;
     return r;
 }
@@ -152,7 +152,7 @@ hipError_t run_rows(int dtype, const RowsProduct &p, const RowsPlan &plan, int64
         a.max_mtiles = (int)moe::max_mtiles_bound(p.M, (int)E, moe::kF32Rows);
         return moe::launch_f32_grouped(p.nt ? moe::F32_NT : moe::F32_NN, a, num_cus, s);
     }
-    if (plan.fast) {
+    if (plan.fast || plan.big) {
         moe::FastFwdArgs a{};
         a.w2 = p.w;
         a.act = const_cast<void *>(p.a);
@@ -168,7 +168,8 @@ hipError_t run_rows(int dtype, const RowsProduct &p, const RowsPlan &plan, int64
         a.K = 1;
         a.max_mtiles = (int)moe::max_mtiles_bound(p.M, (int)E, plan.BM);
         a.drop_mt = -1;
-        return plan.big ? moe::launch_fast_fwd_big(moe::FAST_G2, a, num_cus, s, true)
+        a.lda = (int)p.lda;
+        return plan.big ? moe::launch_grouped_big(p.nt, a, num_cus, s)
                         : moe::launch_fast_fwd(moe::FAST_G2, plan.BM, a, num_cus, s);
     }
     moe::EngineArgs a{};
@@ -280,10 +281,8 @@ int moe_ffn_grouped_mm_bwd(const moe_ffn_grouped *g, const void *dy, const void 
     const int wm = (int)(g->transposed ? g->N : g->Kd), wn = (int)(g->transposed ? g->Kd : g->N);
     const void *a = g->transposed ? dy : x, *b = g->transposed ? x : dy;
     const int64_t lda = g->transposed ? g->N : g->x_stride, ldb = g->transposed ? g->x_stride : g->N;
-    if (d_weight && g->dtype == MOE_FFN_BF16) {
-        set.splits.n = 1;
-        moe::engine_feature_tiling(moe::ENG_GW, wm, wn, num_cus, &set.splits.F[0], &set.splits.wgx[0]);
-    }
+    if (d_weight && g->dtype == MOE_FFN_BF16)
+        set.order = at<int32_t>(ws, L.groups.order);
     HIP_TRY(moe::launch_group_setup(set, s), "group set-up launch");
     if (dx)
         HIP_TRY(run_rows(g->dtype, p, plan, g->E, L.groups, ws, num_cus, s), "input gradient launch");
@@ -316,7 +315,7 @@ int moe_ffn_grouped_mm_bwd(const moe_ffn_grouped *g, const void *dy, const void 
     w.N = wn;
     w.lda = (int)lda;
     w.ldb = (int)ldb;
-    w.xcd_bounds = set.splits.bounds;
+    w.order = set.order;
     HIP_TRY(moe::launch_engine(moe::ENG_GW, 128, w, num_cus, s), "weight gradient launch");
     return MOE_FFN_OK;
 }

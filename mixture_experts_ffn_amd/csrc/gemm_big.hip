@@ -115,14 +115,19 @@ __device__ __forceinline__ float acc_rd(float a)
 // SKIP: waves leave out the copies of token rows that lie past a tile's rows
 // (for launches where many tiles are short: a per-step choice of wait that
 // costs launches of full tiles about 8 %, so it is compiled only where used)
-template <int MODE, bool SKIP>
+// GR: a grouped product on its own (GEMM2's mode): 1 weights [K, N] as in the layer, 2
+// weights [N, K], whose rows are copied and read like token rows.  Either takes any
+// number of columns (a multiple of 8: past the last ones the copies repeat them and
+// nothing is stored) and rows args.lda apart.
+template <int MODE, bool SKIP, int GR>
 __global__ __launch_bounds__(64 * NW, 1) void moe_fwd_bf16_big(FastFwdArgs args)
 {
+    static_assert(GR == 0 || MODE == FAST_G2, "grouped products run as GEMM2");
     __shared__ __attribute__((aligned(1024))) unsigned char smem[NSTAGE * STAGE_BYTES];
     constexpr bool G1 = MODE == FAST_G1 || MODE == FAST_G1H;
     constexpr int KIND = G1 ? KIND_G1 : KIND_G2;
     const int H = args.H, I = args.I;
-    const int ntn = G1 ? I / TILE_N1 : H / TILE_N2;
+    const int ntn = G1 ? I / TILE_N1 : GR ? (H + TILE_N2 - 1) / TILE_N2 : H / TILE_N2;
     const int nk = (G1 ? H : I) / BK;
     const int mtiles = uni(ldc(args.mtile_off, args.E));
     const int per_xcd_wg = gridDim.x >> 3;
@@ -208,7 +213,7 @@ __global__ __launch_bounds__(64 * NW, 1) void moe_fwd_bf16_big(FastFwdArgs args)
     };
     const unsigned char *abase =
         static_cast<const unsigned char *>(G1 ? args.x : args.act); // token rows
-    const int lda = G1 ? H : I;
+    const int lda = GR ? args.lda : G1 ? H : I;
     auto make_src = [&](const Tile &t, Src &sr) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < A_LOADS; ++i) {
@@ -248,7 +253,7 @@ __global__ __launch_bounds__(64 * NW, 1) void moe_fwd_bf16_big(FastFwdArgs args)
                : (shd ? static_cast<const bf16 *>(args.sh.w2) + sc * I * H
                       : static_cast<const bf16 *>(args.w2) + (int64_t)t.e * I * H);
         sr.wbase = reinterpret_cast<const unsigned char *>(W);
-        sr.ldb = G1 ? 2 * (shd ? args.sh.Is : I) : H;
+        sr.ldb = GR == 2 ? 1 : G1 ? 2 * (shd ? args.sh.Is : I) : H; // of a step in k
         // This wave copies token rows A_ROWS * wave .. + A_ROWS - 1.  When they
         // all lie past the tile's rows no wave reads them (the row split
         // below never reaches a 32-row step past the last row), so the wave
@@ -259,11 +264,19 @@ __global__ __launch_bounds__(64 * NW, 1) void moe_fwd_bf16_big(FastFwdArgs args)
         for (int i = 0; i < B_LOADS; ++i) {
             // chunk c covers 1024 bytes = 4 k-rows of one 128-column panel
             const int c = wave * B_LOADS + i;
+            if constexpr (GR == 2) { // RPC weight rows, as the token rows
+                const int r = c * RPC + lane / PIECES;
+                sr.b[i] = (uint32_t)min(t.n0 + r, H - 1) * (uint32_t)(I * 2) +
+                          (uint32_t)(aswz<PIECES>(r, lane % PIECES) * 16);
+                continue;
+            }
             const int panel = c / CPP;
             const int kr = (c % CPP) * 4 + (lane >> 4);
             const int pp = lane & 15;
             const int u = (pp >> 1) ^ bswz(kr);
-            const int col = t.n0 + panel * pstride + (2 * u + (pp & 1)) * 8;
+            int col = t.n0 + panel * pstride + (2 * u + (pp & 1)) * 8;
+            if (GR)
+                col = min(col, H - 8);
             sr.b[i] = (uint32_t)(kr * sr.ldb + col) * 2u;
         }
     };
@@ -319,6 +332,16 @@ __global__ __launch_bounds__(64 * NW, 1) void moe_fwd_bf16_big(FastFwdArgs args)
     };
     auto read_w = [&](WFrag &W, int stage, int p, int q) __attribute__((always_inline)) {
         const int fn = q >> 1, h = q & 1;
+        if constexpr (GR == 2) { // one read for both halves
+            if (h)
+                return;
+            const int r = p * PW + wn * WTN + fn * 16 + fr;
+            const v8i16 v = *reinterpret_cast<const v8i16 *>(
+                smem + stage * STAGE_BYTES + A_BYTES + r * (BK * 2) + aswz<PIECES>(r, fk) * 16);
+            W.h[fn][0] = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+            W.h[fn][1] = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+            return;
+        }
         const unsigned char *sP = smem + stage * STAGE_BYTES + A_BYTES + p * (BK * PW * 2);
         const int nb = wn * WTN + fn * 16 + 4 * tq;
         const int kr = 8 * fk + 4 * h + tr;
@@ -395,7 +418,7 @@ __global__ __launch_bounds__(64 * NW, 1) void moe_fwd_bf16_big(FastFwdArgs args)
             const u32x4 v = *reinterpret_cast<const u32x4 *>(stg + rl * rsb + ((cu ^ (rl & umask)) << 4));
             // h: the tile's up panel (staged columns PW..2PW) goes to the second half
             const int dc = kind == 2 && cu * 8 >= PW ? I - PW : 0;
-            if (local < hrows)
+            if (local < hrows && (!GR || t.n0 + cu * 8 < H))
                 *reinterpret_cast<u32x4 *>(Cout + (int64_t)(t.row0 + hr * split + local) * ldo + t.n0 +
                                            dc + cu * 8) = v;
         }
@@ -568,13 +591,13 @@ __global__ __launch_bounds__(64 * NW, 1) void moe_fwd_bf16_big(FastFwdArgs args)
     }
 }
 
-template <int MODE, bool SKIP>
+template <int MODE, bool SKIP, int GR = 0>
 static hipError_t launch(const FastFwdArgs &a, int num_cus, hipStream_t stream)
 {
     // one workgroup per CU, whole XCDs
     const int grid = a.grid > 0 ? a.grid : (num_cus + 7) / 8 * 8;
-    hipLaunchKernelGGL((moe_fwd_bf16_big<MODE, SKIP>), dim3((unsigned)grid), dim3(64 * NW), 0, stream,
-                       a);
+    hipLaunchKernelGGL((moe_fwd_bf16_big<MODE, SKIP, GR>), dim3((unsigned)grid), dim3(64 * NW), 0,
+                       stream, a);
     return hipGetLastError();
 }
 
@@ -593,6 +616,14 @@ hipError_t launch_fast_fwd_big(int mode, const FastFwdArgs &a, int num_cus, hipS
                             : big::launch<FAST_G2, false>(a, num_cus, stream);
     default: return hipErrorInvalidValue;
     }
+}
+
+hipError_t launch_grouped_big(bool nt, const FastFwdArgs &a, int num_cus, hipStream_t stream)
+{
+    if (a.T <= 0)
+        return hipSuccess;
+    return nt ? big::launch<FAST_G2, true, 2>(a, num_cus, stream)
+              : big::launch<FAST_G2, true, 1>(a, num_cus, stream);
 }
 
 } // namespace moe

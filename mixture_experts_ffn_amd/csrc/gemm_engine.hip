@@ -206,6 +206,36 @@ __device__ __forceinline__ int ldc(const int32_t *p, int i)
     return ((const __attribute__((address_space(4))) int32_t *)p)[uni(i)];
 }
 
+// GW's walk.  A tile's cost follows its group's rows, which the caller's routing may
+// skew, so the groups come by descending rows (a.order), the F tiles of each are
+// shared out over the XCDs in runs of an eighth of them (so that a run still shares
+// operands in an L2), and an XCD's workgroups walk its tiles up and down in turns,
+// so that who gets a dear tile of one round gets a cheap one of the next.  L counts
+// whole rounds of the XCD's workgroups; past the last tile rank is E or more.
+struct GwPlace {
+    int rank, tile;
+};
+__device__ __forceinline__ GwPlace gw_place(const EngineArgs &a, int L, int F)
+{
+    const int wgx = gridDim.x >> 3, xcd = blockIdx.x & 7;
+    const int j = L / wgx, s = L - j * wgx;
+    const int p = j * wgx + ((j & 1) ? wgx - 1 - s : s); // place among the XCD's tiles
+    const int run = (F + 7) >> 3, r = p / run;
+    const int id = (xcd + 8 * r) * run + p - r * run;
+    GwPlace g;
+    g.rank = uni(id / F);
+    g.tile = uni(id - g.rank * F);
+    return g;
+}
+// whole rounds that cover the XCD's tiles
+__device__ __forceinline__ int gw_end(const EngineArgs &a, int F)
+{
+    const int wgx = gridDim.x >> 3, xcd = blockIdx.x & 7;
+    const int run = (F + 7) >> 3, runs = (a.E * F + run - 1) / run;
+    const int mine = (runs - xcd + 7) >> 3;
+    return (mine * run + wgx - 1) / wgx * wgx;
+}
+
 // All fields are wave-uniform; readfirstlane keeps the decode on the scalar
 // unit (scalar loads, tracked by lgkmcnt) so it never waits for the copies in
 // flight on the vector-memory counter.
@@ -235,8 +265,17 @@ __device__ __forceinline__ TileInfo decode_tile(const EngineArgs &a, int L)
         t.klen = a.Kd;
     } else {
         const int mtm = (a.M + BM - 1) / BM, ntn = (a.N + C::OUT_N - 1) / C::OUT_N;
-        t.e = L / (mtm * ntn);
-        const int local = L - t.e * mtm * ntn;
+        int local;
+        bool past = false;
+        if constexpr (KIND == GW) {
+            const GwPlace g = gw_place(a, L, mtm * ntn);
+            past = g.rank >= a.E;
+            t.e = past ? 0 : ldc(a.order, g.rank);
+            local = g.tile;
+        } else {
+            t.e = L / (mtm * ntn);
+            local = L - t.e * mtm * ntn;
+        }
         // groups of GM feature tiles, N outer: the 32 tiles in flight on one
         // XCD then span 8 M-tiles x 4 N-tiles of one expert (their operand
         // blocks fit its L2) instead of 32 M-tiles of one N-tile
@@ -251,6 +290,10 @@ __device__ __forceinline__ TileInfo decode_tile(const EngineArgs &a, int L)
         t.n0 = n_t * C::OUT_N;
         t.seg0 = ldc(a.offsets, t.e);
         t.klen = ldc(a.offsets, t.e + 1) - t.seg0;
+        if (past) { // behind the last tile: nothing to sum or store
+            t.rows = 0;
+            t.klen = 0;
+        }
     }
     t.e = uni(t.e);
     t.m0 = uni(t.m0);
@@ -281,6 +324,11 @@ template <int KIND, int BM, int WM>
 __device__ __forceinline__ void xcd_range(const EngineArgs &a, int x, int &lo, int &hi)
 {
     using C = Cfg<KIND, BM, WM>;
+    if constexpr (KIND == GW) {
+        lo = 0;
+        hi = gw_end(a, ((a.M + BM - 1) / BM) * ((a.N + C::OUT_N - 1) / C::OUT_N));
+        return;
+    }
     if constexpr (!C::KT::TOKEN_M) {
         if (a.xcd_bounds) {
             lo = ldc(a.xcd_bounds, x);
@@ -996,10 +1044,8 @@ void engine_feature_tiling(int kind, int M, int N, int num_cus, int *tiles_per_e
 {
     using namespace eng;
     // the weight-gradient kinds launch with 128-row feature tiles (launch_engine)
-    const int out_n = kind == ENG_B5 ? Cfg<B5, 128, 2>::OUT_N
-                      : kind == ENG_B7 ? Cfg<B7, 128, 2>::OUT_N
-                                       : Cfg<GW, 128, 2>::OUT_N;
-    const int wgpc = kind == ENG_B5 ? Shape<B5>::WGPC : kind == ENG_B7 ? Shape<B7>::WGPC : Shape<GW>::WGPC;
+    const int out_n = kind == ENG_B5 ? Cfg<B5, 128, 2>::OUT_N : Cfg<B7, 128, 2>::OUT_N;
+    const int wgpc = kind == ENG_B5 ? Shape<B5>::WGPC : Shape<B7>::WGPC;
     *tiles_per_expert = ((M + 127) / 128) * ((N + out_n - 1) / out_n);
     *wg_per_xcd = (num_cus + 7) / 8 * wgpc;
 }

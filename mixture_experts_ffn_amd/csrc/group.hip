@@ -4,13 +4,12 @@
 // One block forms, of offsets that may hold anything, o'[e] = max over e' <= e of
 // offsets[e'] held to [0, M]: ascending and inside the rows, so that no later
 // kernel indexes outside them, and equal to valid offsets.  From these it builds the
-// M-tile tables (prefix of ceil(rows / BM), owner of every tile) and the bounds of
-// the weight gradient's XCDs.  The other blocks zero the output rows that belong
-// to no group, which no GEMM tile covers.  A launch of 4 us: the scan's two
-// barriers and one dependent load each way.
+// M-tile tables (prefix of ceil(rows / BM), owner of every tile) and the groups'
+// order by their rows, for the weight gradient.  The other blocks zero the output
+// rows that belong to no group, which no GEMM tile covers.  A launch of 4 us: the
+// scans' barriers and one dependent load each way.
 #include "common.h"
 #include "kernels.h"
-#include "xcd_split.h"
 
 namespace moe {
 
@@ -47,7 +46,7 @@ template <typename Op> __device__ inline int32_t block_scan(int32_t v, int32_t *
 
 __global__ __launch_bounds__(kSetupThreads) void group_setup_kernel(GroupSetup g)
 {
-    __shared__ int32_t s_off[1025], s_moff[1025], s_w[16], s_raw[2][8];
+    __shared__ int32_t s_off[1025], s_moff[1025], s_w[16];
     const int t = threadIdx.x, E = g.E;
     const int32_t raw = t <= E ? held_offset(g, t) : 0;
     const int32_t o = block_scan(raw, s_w, [](int32_t a, int32_t b) { return max(a, b); });
@@ -95,7 +94,15 @@ __global__ __launch_bounds__(kSetupThreads) void group_setup_kernel(GroupSetup g
         }
         g.mtile_expert[j] = lo;
     }
-    xcd_split(s_off, E, g.splits, s_raw);
+    if (g.order && t < E) { // descending by rows, equals by number
+        const int32_t rows = s_off[t + 1] - s_off[t];
+        int rank = 0;
+        for (int e = 0; e < E; ++e) {
+            const int32_t other = s_off[e + 1] - s_off[e];
+            rank += other > rows || (other == rows && e < t);
+        }
+        g.order[rank] = t;
+    }
 }
 
 hipError_t launch_group_setup(const GroupSetup &g, hipStream_t s)

@@ -158,6 +158,7 @@ struct FastFwdArgs {
     int max_mtiles;
     int drop_mt;                 // test hook: M-tile whose first GEMM1 release is dropped (-1)
     SharedExperts sh;            // E counts the shared chunks too (sh.Er routed)
+    int lda;                     // launch_grouped_big: elements from one row to the next
 };
 enum { FAST_G1 = 0, FAST_G2 = 1, FAST_PIPE = 2, FAST_G1H = 3 }; // FAST_G1H: FAST_G1 saving h
 hipError_t launch_fast_fwd(int mode, int BM, const FastFwdArgs &a, int num_cus,
@@ -169,6 +170,9 @@ hipError_t launch_fast_fwd(int mode, int BM, const FastFwdArgs &a, int num_cus,
 // rows, for launches where many tiles are short
 hipError_t launch_fast_fwd_big(int mode, const FastFwdArgs &a, int num_cus, hipStream_t stream,
                                bool skip_padding = false);
+// a grouped product on the same kernel: o [T, H] = act [T, I] (rows lda apart) . w2[e],
+// w2 [E, I, H], or [E, H, I] if nt; I a multiple of 32 and 128 at least, H of 8
+hipError_t launch_grouped_big(bool nt, const FastFwdArgs &a, int num_cus, hipStream_t stream);
 
 // bf16 engine (gemm_engine.hip): forward F1/F2, backward B2/B4/B5/B7 and the
 // grouped products' weight gradient GW
@@ -206,11 +210,12 @@ struct EngineArgs {
     // feature-tiled kinds, optional: [9] tile bounds of the eight XCDs (from
     // the backward set-up); null: an eighth of the tiles each
     const int32_t *xcd_bounds;
+    const int32_t *order;        // GW: [E] groups by descending rows
 };
 enum { ENG_F1 = 0, ENG_F2 = 1, ENG_B2 = 2, ENG_B4 = 3, ENG_B5 = 4, ENG_B7 = 5, ENG_GW = 6 };
 hipError_t launch_engine(int kind, int BM, const EngineArgs &a, int num_cus, hipStream_t stream);
 int engine_dgp_width(int I); // columns of the B2 partial-dot buffer
-// a weight-gradient kind's (ENG_B5, ENG_B7, ENG_GW) feature tiles per expert for an
+// a weight-gradient kind's (ENG_B5 / ENG_B7) feature tiles per expert for an
 // M x N gradient, and its workgroups per XCD
 void engine_feature_tiling(int kind, int M, int N, int num_cus, int *tiles_per_expert,
                            int *wg_per_xcd);
@@ -241,19 +246,10 @@ struct MxGemmArgs {
 };
 hipError_t launch_mx_gemm(bool g1, int bits, const MxGemmArgs &a, int num_cus, hipStream_t s);
 
-// Bounds of a cost-balanced split of weight-gradient tiles over the XCDs.
-struct XcdSplits {
-    int n;          // launches (0..2)
-    int F[2];       // feature tiles per expert
-    int wgx[2];     // workgroups per XCD
-    int32_t *bounds; // [n][9]
-};
-
 // ---- row groups by offsets (group.hip) ---------------------------------------------
 // What the grouped products' kernels read, from a caller's offsets: checked
-// offsets, M-tile tables of BM rows (and of BM2, if not 0), the bounds of the
-// weight gradient's XCDs, zeroed tickets; and zeros in the rows of up to two
-// outputs that belong to no group.
+// offsets, M-tile tables of BM rows, the groups by descending rows, zeroed
+// tickets; and zeros in the output rows that belong to no group.
 struct GroupSetup {
     const void *offsets;          // [E + 1]; null: one group of all M rows
     bool off64;
@@ -262,7 +258,7 @@ struct GroupSetup {
     int32_t *out_offsets;         // [E + 1]
     int32_t *mtile_off, *mtile_expert;
     int32_t *tickets;             // [16]
-    XcdSplits splits;
+    int32_t *order;               // [E], or null
     void *out;                    // null: none
     int64_t out_row;              // bytes of an output row, a multiple of 16
 };
@@ -360,6 +356,12 @@ hipError_t launch_zero_fill(void *p, size_t bytes, hipStream_t stream);
 // nine tile bounds of a cost-balanced split over the eight XCDs into
 // xcd_bounds[9 i .. 9 i + 8].
 enum { BWD_STAGE_ALL = 0, BWD_STAGE_D = 1, BWD_STAGE_W = 2 };
+struct XcdSplits {
+    int n;          // launches (0..2)
+    int F[2];       // feature tiles per expert
+    int wgx[2];     // workgroups per XCD
+    int32_t *bounds; // [n][9]
+};
 hipError_t launch_bwd_setup(const SavedHeader *hdr, uint64_t problem_hash, const int32_t *counts,
                             const int32_t *offsets, int E, int64_t TK, int BM, int32_t *counts_out,
                             int32_t *offsets_out, int32_t *mtile_off, int32_t *mtile_expert,
