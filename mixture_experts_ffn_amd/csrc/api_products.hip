@@ -27,7 +27,7 @@ struct Taker {
 
 // What the grouped kernels walk, in a workspace (group.hip).
 struct GroupLayout {
-    size_t offsets, mtile_off, mtile_expert, tickets, order;
+    size_t offsets, mtile_off, mtile_expert, tickets, order, alt_off, alt_expert;
     int64_t max_mtiles;
     void lay(Taker &take, int64_t M, int64_t E, int min_rows)
     {
@@ -37,6 +37,9 @@ struct GroupLayout {
         mtile_expert = take(sizeof(int32_t) * (size_t)max_mtiles);
         tickets = take(sizeof(int32_t) * 16);
         order = take(sizeof(int32_t) * (size_t)E);
+        // second tables: 128-row tiles
+        alt_off = take(sizeof(int32_t) * (size_t)(E + 1));
+        alt_expert = take(sizeof(int32_t) * (size_t)moe::max_mtiles_bound(M, (int)E, 128));
     }
     moe::GroupSetup setup(void *ws, const void *given, int offsets_dtype, int64_t M, int64_t E, int BM) const
     {
@@ -113,21 +116,33 @@ struct RowsProduct {
     bool nt;
 };
 
-// The kernel and the tile height for a product, by the mean rows of a group.
+// The kernels and the tile heights for a product, by the mean rows of a group: up to
+// 64 tiles of 64 rows, up to 256 of 128, from there on by the model in kernels.h: for
+// what the host knows, routed rows that split evenly, or, where a product is long
+// beside a launch (a skewed routing decides 10 % of it), by the set-up kernel.
 struct RowsPlan {
-    int BM;
-    bool fast, big;
+    int BM;          // rows of an M-tile; both: of the first tables
+    bool fast;       // gemm_mfma.hip serves the low tiles
+    bool big, both;  // 256-row tiles; either, as the set-up decides
+    moe::TileModel model;
 };
-RowsPlan plan_rows(int dtype, const RowsProduct &p, int64_t E)
+RowsPlan plan_rows(int dtype, const RowsProduct &p, int64_t E, int num_cus)
 {
-    RowsPlan r{64, false, false};
+    RowsPlan r{64, false, false, false, {}};
     if (dtype == MOE_FFN_F32)
         return r; // moe::kF32Rows
     const double rows = (double)p.M / (double)E;
-    r.big = rows > 256 && p.K % 32 == 0 && p.K >= 128 &&
-            p.M * p.lda * 2 < (int64_t(1) << 32); // 32-bit row offsets
-    r.fast = !r.big && !p.nt && p.lda == p.K && moe::fast_gemm_supported(1, p.N, p.K);
-    r.BM = r.big ? 256 : rows <= 64 ? 64 : 128;
+    r.fast = !p.nt && p.lda == p.K && moe::fast_gemm_supported(1, p.N, p.K);
+    r.BM = rows <= 64 ? 64 : 128;
+    if (rows > 256 && p.K % 32 == 0 && p.K >= 128 &&
+        p.M * p.lda * 2 < (int64_t(1) << 32)) { // 32-bit row offsets
+        r.model = {(float)((p.N + 255) / 256) / (float)num_cus, r.fast};
+        r.both = E > 1 && (double)p.M * (double)p.N * (double)p.K > 6e10; // 100 us and more
+        r.big = r.both || moe::tall_tiles(r.model, (float)p.M, (float)p.M / 256 + 0.5f * (float)E,
+                                          (float)p.M / 128 + 0.5f * (float)E);
+    }
+    if (r.big)
+        r.BM = 256;
     return r;
 }
 
@@ -152,25 +167,32 @@ hipError_t run_rows(int dtype, const RowsProduct &p, const RowsPlan &plan, int64
         a.max_mtiles = (int)moe::max_mtiles_bound(p.M, (int)E, moe::kF32Rows);
         return moe::launch_f32_grouped(p.nt ? moe::F32_NT : moe::F32_NN, a, num_cus, s);
     }
-    if (plan.fast || plan.big) {
-        moe::FastFwdArgs a{};
-        a.w2 = p.w;
-        a.act = const_cast<void *>(p.a);
-        a.o = p.out;
-        a.offsets = offsets;
-        a.mtile_off = mtile_off;
-        a.mtile_expert = mtile_expert;
-        a.tickets = at<int32_t>(ws, G.tickets);
-        a.T = (int)p.M;
-        a.H = (int)p.N;
-        a.I = (int)p.K;
-        a.E = (int)E;
-        a.K = 1;
-        a.max_mtiles = (int)moe::max_mtiles_bound(p.M, (int)E, plan.BM);
-        a.drop_mt = -1;
-        a.lda = (int)p.lda;
-        return plan.big ? moe::launch_grouped_big(p.nt, a, num_cus, s)
-                        : moe::launch_fast_fwd(moe::FAST_G2, plan.BM, a, num_cus, s);
+    moe::FastFwdArgs f{};
+    f.w2 = p.w;
+    f.act = const_cast<void *>(p.a);
+    f.o = p.out;
+    f.offsets = offsets;
+    f.mtile_off = mtile_off;
+    f.mtile_expert = mtile_expert;
+    f.tickets = at<int32_t>(ws, G.tickets);
+    f.T = (int)p.M;
+    f.H = (int)p.N;
+    f.I = (int)p.K;
+    f.E = (int)E;
+    f.K = 1;
+    f.drop_mt = -1;
+    f.lda = (int)p.lda;
+    if (plan.big) {
+        const hipError_t err = moe::launch_grouped_big(p.nt, f, num_cus, s);
+        if (err != hipSuccess || !plan.both)
+            return err;
+        mtile_off = f.mtile_off = at<int32_t>(ws, G.alt_off);
+        mtile_expert = f.mtile_expert = at<int32_t>(ws, G.alt_expert);
+    }
+    const int BM = plan.big ? 128 : plan.BM;
+    if (plan.fast) {
+        f.max_mtiles = (int)moe::max_mtiles_bound(p.M, (int)E, BM);
+        return moe::launch_fast_fwd(moe::FAST_G2, BM, f, num_cus, s);
     }
     moe::EngineArgs a{};
     a.A = static_cast<const moe::bf16_t *>(p.a);
@@ -188,7 +210,17 @@ hipError_t run_rows(int dtype, const RowsProduct &p, const RowsPlan &plan, int64
     a.ldb = (int)(p.nt ? p.K : p.N);
     a.ldc = (int)p.N;
     a.b_estride = p.K * p.N;
-    return moe::launch_engine(p.nt ? moe::ENG_B4 : moe::ENG_F2, plan.BM, a, num_cus, s);
+    return moe::launch_engine(p.nt ? moe::ENG_B4 : moe::ENG_F2, BM, a, num_cus, s);
+}
+
+// The set-up's side of a plan.
+void set_plan(moe::GroupSetup &set, const RowsPlan &plan, const GroupLayout &G, void *ws)
+{
+    if (!plan.both)
+        return;
+    set.alt.mtile_off = at<int32_t>(ws, G.alt_off);
+    set.alt.mtile_expert = at<int32_t>(ws, G.alt_expert);
+    set.alt.model = plan.model;
 }
 
 } // namespace
@@ -228,8 +260,9 @@ int moe_ffn_grouped_mm(const moe_ffn_grouped *g, const void *x, const void *weig
         return rc;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const RowsProduct p{x, weight, y, g->M, g->Kd, g->N, g->x_stride, g->transposed == 1};
-    const RowsPlan plan = plan_rows(g->dtype, p, g->E);
+    const RowsPlan plan = plan_rows(g->dtype, p, g->E, num_cus);
     moe::GroupSetup set = L.groups.setup(ws, offsets, g->offsets_dtype, g->M, g->E, plan.BM);
+    set_plan(set, plan, L.groups, ws);
     set.out = y;
     set.out_row = g->N * (int64_t)elem_size(g->dtype);
     HIP_TRY(moe::launch_group_setup(set, s), "group set-up launch");
@@ -273,8 +306,9 @@ int moe_ffn_grouped_mm_bwd(const moe_ffn_grouped *g, const void *dy, const void 
         return MOE_FFN_OK;
     // dx = dy . W^T: the weights are read along the other axis than the forward's
     const RowsProduct p{dy, weight, dx, g->M, g->N, g->Kd, g->N, g->transposed == 0};
-    const RowsPlan plan = plan_rows(g->dtype, p, g->E);
+    const RowsPlan plan = plan_rows(g->dtype, p, g->E, num_cus);
     moe::GroupSetup set = L.groups.setup(ws, offsets, g->offsets_dtype, g->M, g->E, plan.BM);
+    set_plan(set, plan, L.groups, ws);
     set.out = dx;
     set.out_row = g->Kd * (int64_t)item;
     // the weight's gradient: a^T b with a's columns the weight's rows

@@ -72,27 +72,47 @@ __global__ __launch_bounds__(kSetupThreads) void group_setup_kernel(GroupSetup g
         g.out_offsets[E] = s_off[E];
     if (t < 16)
         g.tickets[t] = 0;
-    const int32_t tiles = t < E ? (s_off[t + 1] - s_off[t] + g.BM - 1) / g.BM : 0;
-    const int32_t upto = block_scan(tiles, s_w, [](int32_t a, int32_t b) { return a + b; });
-    if (t < E) {
-        s_moff[t + 1] = upto;
-        g.mtile_off[t + 1] = upto;
-    }
-    if (t == 0) {
-        s_moff[0] = 0;
-        g.mtile_off[0] = 0;
-    }
-    __syncthreads();
-    for (int j = t; j < s_moff[E]; j += kSetupThreads) {
-        int lo = 0, hi = E; // the group e with moff[e] <= j < moff[e + 1]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (s_moff[mid] <= j)
-                lo = mid;
-            else
-                hi = mid;
+    auto sum = [](int32_t a, int32_t b) { return a + b; };
+    auto tiles_of = [&](int BM) { return t < E ? (s_off[t + 1] - s_off[t] + BM - 1) / BM : 0; };
+    // M-tiles of BM rows into a table, or, if not `used`, none
+    auto table = [&](int BM, int32_t *off, int32_t *owner, bool used) {
+        const int32_t upto = block_scan(used ? tiles_of(BM) : 0, s_w, sum);
+        if (t < E) {
+            s_moff[t + 1] = upto;
+            off[t + 1] = upto;
         }
-        g.mtile_expert[j] = lo;
+        if (t == 0) {
+            s_moff[0] = 0;
+            off[0] = 0;
+        }
+        __syncthreads();
+        for (int m = t; m < s_moff[E]; m += kSetupThreads) {
+            int lo = 0, hi = E; // the group e with moff[e] <= m < moff[e + 1]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (s_moff[mid] <= m)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            owner[m] = lo;
+        }
+    };
+    if (!g.alt.mtile_off) {
+        table(g.BM, g.mtile_off, g.mtile_expert, true);
+    } else {
+        __shared__ int32_t s_tiles[2];
+        const int32_t a = block_scan(tiles_of(256), s_w, sum), b = block_scan(tiles_of(128), s_w, sum);
+        if (t == kSetupThreads - 1) {
+            s_tiles[0] = a;
+            s_tiles[1] = b;
+        }
+        __syncthreads();
+        const float rows = (float)(s_off[E] - s_off[0]);
+        const bool tall = tall_tiles(g.alt.model, rows, (float)s_tiles[0], (float)s_tiles[1]);
+        table(256, g.mtile_off, g.mtile_expert, tall);
+        __syncthreads(); // s_moff is read
+        table(128, g.alt.mtile_off, g.alt.mtile_expert, !tall);
     }
     if (g.order && t < E) { // descending by rows, equals by number
         const int32_t rows = s_off[t + 1] - s_off[t];

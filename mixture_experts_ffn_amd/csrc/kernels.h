@@ -246,6 +246,32 @@ struct MxGemmArgs {
 };
 hipError_t launch_mx_gemm(bool g1, int bits, const MxGemmArgs &a, int num_cus, hipStream_t s);
 
+// ---- tile height of the grouped bf16 products -------------------------------------
+// From 256 mean rows of a group on: 256 x 256 tiles (gemm_big.hip, one workgroup a
+// CU), or 128 x 256 (gemm_mfma.hip, two a CU, for whole tiles of [K, N] weights; else
+// gemm_engine.hip, one), by a model of their rounds over the CUs.  A 256-row tile with
+// few rows costs 0.8 of a full one; two 128-row tiles of gemm_mfma.hip 1.06 of it, a
+// last round that leaves it one workgroup a CU 0.62 of a whole one; a tile of the
+// engine 0.57.  Both sides in us (256 : 128 rows; [K, N], [N, K] weights): 16384 x 1024
+// x 1024 over 8 groups 66 : 55, 66 : 59; 8192 x 4096 x 8192 over 4 540 : 482, 555 : 561;
+// 24576 x 2816 x 2048 over 64 310 : 341, 325 : 355, and with rows by Zipf's law 388 : 350,
+// 403 : 351; 32768 x 7168 x 4096 over 16 1755 : 1966, 1865 : 1964.  Of 18 such sizes the
+// model picks the slower side once, 5 % off.
+struct TileModel {
+    float columns; // column tiles over CUs
+    bool two;      // the 128-row side is gemm_mfma.hip
+};
+__host__ __device__ inline bool tall_tiles(const TileModel &m, float rows, float tiles256, float tiles128)
+{
+    const float full = rows / (256.f * (tiles256 > 1.f ? tiles256 : 1.f));
+    const float r = tiles256 * m.columns; // from six rounds on the last two go by tickets
+    const float tall = (r > 5.f ? r + 0.3f : __builtin_ceilf(r)) * (0.8f + 0.2f * full);
+    const float f = 0.5f * tiles128 * m.columns, part = f - __builtin_floorf(f);
+    const float low = m.two ? 1.06f * (__builtin_floorf(f) + (part > 0.5f ? 1.f : part > 0.f ? 0.62f : 0.f))
+                            : 0.57f * __builtin_ceilf(2.f * f);
+    return tall < low;
+}
+
 // ---- row groups by offsets (group.hip) ---------------------------------------------
 // What the grouped products' kernels read, from a caller's offsets: checked
 // offsets, M-tile tables of BM rows, the groups by descending rows, zeroed
@@ -258,6 +284,12 @@ struct GroupSetup {
     int32_t *out_offsets;         // [E + 1]
     int32_t *mtile_off, *mtile_expert;
     int32_t *tickets;             // [16]
+    // Optional: the first tables hold tiles of 256 rows and these of 128, and the model
+    // leaves one of the two empty, whose launch then ends at once.
+    struct {
+        int32_t *mtile_off, *mtile_expert;
+        TileModel model;
+    } alt;
     int32_t *order;               // [E], or null
     void *out;                    // null: none
     int64_t out_row;              // bytes of an output row, a multiple of 16
