@@ -757,13 +757,20 @@ int moe_ffn_int8_fwd(const moe_ffn_problem *p, const void *x, const void *topk_i
     rb.sorted_slot = at<int32_t>(ws, L.sorted_slot);
     rb.slot_pos = at<int32_t>(ws, L.slot_pos);
     rb.T = p->T;
-    HIP_TRY(moe::launch_route(topk_ids, p->ids_dtype == MOE_FFN_I64, TK, E, L.BM, L.rp, rb, s),
+    // the token rows by further blocks of the routing launch, which they keep in
+    // registers, or by a launch of their own
+    const moe::MxRows rows{x, at<void>(ws, L.x_codes), nullptr, at<void>(ws, L.x_scales), p->T,
+                           (int)p->H, 0, (int)moe::I8Dims(p->H, 8).row(), 8};
+    const bool ride = p->H <= moe::kRideMaxH;
+    HIP_TRY(moe::launch_route(topk_ids, p->ids_dtype == MOE_FFN_I64, TK, E, L.BM, L.rp, rb, s,
+                              ride ? &rows : nullptr),
             "route launch");
+    if (!ride)
+        HIP_TRY(moe::launch_i8_quantize_rows(MOE_FFN_BF16, x, p->H, rows.codes,
+                                             static_cast<float *>(rows.scales), p->T, p->H, s),
+                "token quantisation launch");
     if ((flags & MOE_FFN_CHECK_IDS) && (rc = check_ids(rb.status, E, s)))
         return rc;
-    HIP_TRY(moe::launch_i8_quantize_rows(MOE_FFN_BF16, x, p->H, at<void>(ws, L.x_codes),
-                                         at<float>(ws, L.x_scales), p->T, p->H, s),
-            "token quantisation launch");
 
     moe::I8GemmArgs g{};
     g.sorted_slot = rb.sorted_slot;

@@ -4,8 +4,6 @@
 // A vector's codes need its largest magnitude first: a workgroup or a wave holds its
 // vectors in registers between the two, where they fit.  Bound by HBM: a weight of n
 // values moves 2n (or 4n) + n bytes, a row of Kd 2 Kd (or 4 Kd) + Kd.
-#include <type_traits>
-
 #include "i8.h"
 #include "kernels.h"
 
@@ -246,92 +244,13 @@ __global__ __launch_bounds__(64 * kI8Waves) void i8_dequantize_weight_kernel(
     }
 }
 
-// Token rows.  W waves a row: one where there are many rows, or rows that it covers in
-// one step, else the whole workgroup, whose waves then exchange their maxima.  Rows
-// of up to HELD steps (of 512 W values) stay in registers between the maximum and the
-// codes; 0: longer ones, read twice.  24576 x 1408 bf16 18 us (5.7 TB/s), 8192 x 7168 28
-// (6.3), 65536 x 2048 fp32 129 (5.2).
-template <typename T> struct I8Eight {
-    u32x4 v[sizeof(T) / 2]; // eight values
-};
 template <typename T, int W, int HELD>
 __global__ __launch_bounds__(256) void i8_quantize_rows_kernel(const T *__restrict__ x, int64_t stride,
                                                                uint8_t *__restrict__ codes,
                                                                float *__restrict__ scales, int64_t M,
                                                                int Kd, int row_bytes)
 {
-    __shared__ uint32_t s_top[4];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int me = (W == 4 ? threadIdx.x : lane) * 8; // Kd is a multiple of 8
-    constexpr int STEP = 512 * W;
-    for (int64_t m = W == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + wave; m < M;
-         m += (int64_t)gridDim.x * (4 / W)) {
-        const T *row = x + m * stride;
-        I8Eight<T> held[HELD ? HELD : 1];
-        auto load = [&](int k, I8Eight<T> &d) {
-            d = I8Eight<T>{};
-            if (k < Kd)
-                d = *reinterpret_cast<const I8Eight<T> *>(row + k);
-        };
-        std::conditional_t<sizeof(T) == 2, I8Top2, I8Top<float>> tops;
-        auto maximum = [&](const I8Eight<T> &d) {
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(T) * 2; ++i)
-                if constexpr (sizeof(T) == 2)
-                    tops.add(d.v[0][i]);
-                else
-                    tops.add(__uint_as_float(d.v[i >> 2][i & 3]));
-        };
-        if constexpr (HELD > 0) {
-#pragma unroll
-            for (int i = 0; i < HELD; ++i)
-                load(me + i * STEP, held[i]);
-#pragma unroll
-            for (int i = 0; i < HELD; ++i)
-                maximum(held[i]);
-        } else {
-            for (int k = me; k < Kd; k += STEP) {
-                load(k, held[0]);
-                maximum(held[0]);
-            }
-        }
-        uint32_t top = tops.bits();
-#pragma unroll
-        for (int d = 32; d >= 1; d >>= 1)
-            top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
-        if constexpr (W == 4) {
-            __syncthreads(); // the last row's maxima are read
-            if (lane == 0)
-                s_top[wave] = top;
-            __syncthreads();
-            top = max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3]));
-        }
-        const I8Scale s = i8_scale<T>(top);
-        if (me == 0)
-            scales[m] = s.scale;
-        uint8_t *out = codes + m * row_bytes;
-        auto store = [&](int k, const I8Eight<T> &d) {
-            const T *p = reinterpret_cast<const T *>(&d);
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = to_f32<T>(p[i]); // zeros behind Kd
-            u32x2 c;
-            i8_codes<T, 8>(v, s, reinterpret_cast<uint32_t *>(&c));
-            if (k < row_bytes)
-                *reinterpret_cast<u32x2 *>(out + k) = c;
-        };
-        if constexpr (HELD > 0) {
-#pragma unroll
-            for (int i = 0; i < HELD; ++i)
-                store(me + i * STEP, held[i]);
-        } else {
-            for (int k = me; k < row_bytes; k += STEP) {
-                load(k, held[0]);
-                store(k, held[0]);
-            }
-        }
-    }
+    i8_quantize_rows<T, W, HELD, 4>(x, stride, codes, scales, M, Kd, row_bytes, blockIdx.x, gridDim.x);
 }
 
 static dim3 weight_grid(const I8Dims &d, int64_t E, int panels)

@@ -73,14 +73,16 @@ struct RouteBufs {
 enum { MOE_DEV_BAD_ID = 1, MOE_DEV_TIMEOUT = 2, MOE_DEV_BAD_SAVED = 4, MOE_DEV_BAD_WS = 8 };
 
 
-// Token rows x [T, H] bf16 to be quantised to codes of `bits` (4 or 6) bits,
-// row-major (mx.h)
+// Token rows x [T, H] bf16 to be quantised to codes of `bits` bits, row-major: 4 or 6
+// (mx.h), or 8 (i8.h: one fp32 scale a row, srow bytes of codes a row, H up to
+// kRideMaxH)
 struct MxRows {
     const void *x;
     void *codes, *tails, *scales; // tails: 6 bits only
     int64_t T;
     int H, KS, srow, bits;
 };
+constexpr int kRideMaxH = 8192;
 
 RoutePlan make_route_plan(int64_t TK, int E);
 // rows: token rows that are quantised by further blocks of the routing launch

@@ -32,6 +32,7 @@
 // experts the per-block table would not fit either, and hist, scan and
 // scatter run as three launches.
 #include "common.h"
+#include "i8.h"
 #include "kernels.h"
 #include "mx.h"
 
@@ -384,8 +385,8 @@ __global__ __launch_bounds__(64) void route_scatter_kernel(
 // per-(expert, chunk) bases; block 0 also publishes counts, offsets, the
 // M-tile tables and the status word.  LDS: tab[E][16], tot[E], bef[E] (and
 // aft[E] in ROUTE_SELF).
-// RIDE = 4 or 6: blocks from `nblk` on quantise token rows to that many bits
-// instead.  Routing leaves nearly all of the chip idle and the rows need nothing
+// RIDE = 4, 6 or 8: blocks from `nblk` on quantise token rows to that many bits
+// instead (8: four waves a row).  Routing leaves nearly all of the chip idle and the rows need nothing
 // of it, so the two take the time of the longer one and a launch less (one token
 // of 7168: 5.6 us against 5.4 + 2.0, 128 tokens: 6.4 against 7.0 + 4.7, 4096 of
 // 2048: 13 against 12 + 6.5).
@@ -404,11 +405,19 @@ __global__ __launch_bounds__(1024) void route_block_kernel(
 {
     if constexpr (RIDE != 0) {
         if ((int)blockIdx.x >= nblk) {
-            const int64_t n = rows.T * (2 * rows.KS);
-            const int64_t step = (int64_t)(gridDim.x - nblk) * 1024;
-            for (int64_t i = (int64_t)(blockIdx.x - nblk) * 1024 + threadIdx.x; i < n; i += step)
-                mx_quantize_block<RIDE>(rows, i);
-            return;
+            if constexpr (RIDE == 8) {
+                i8_quantize_rows<bf16, 4, 4, 16>(static_cast<const bf16 *>(rows.x), rows.H,
+                                                 static_cast<uint8_t *>(rows.codes),
+                                                 static_cast<float *>(rows.scales), rows.T, rows.H,
+                                                 rows.srow, blockIdx.x - nblk, gridDim.x - nblk);
+                return;
+            } else {
+                const int64_t n = rows.T * (2 * rows.KS);
+                const int64_t step = (int64_t)(gridDim.x - nblk) * 1024;
+                for (int64_t i = (int64_t)(blockIdx.x - nblk) * 1024 + threadIdx.x; i < n; i += step)
+                    mx_quantize_block<RIDE>(rows, i);
+                return;
+            }
         }
     }
     extern __shared__ int32_t lds[];
@@ -790,8 +799,11 @@ static hipError_t launch_route_t(const Id *ids, int64_t TK, int E, int BM, const
                                rp.RC, rp.NB, rb.hist, rb.bad);
         auto kern = !rows             ? route_block<Id, 0>(mode)
                     : rows->bits == 4 ? route_block<Id, 4>(mode)
-                                      : route_block<Id, 6>(mode);
-        const int64_t ride = rows ? (rows->T * rows->KS * 2 + 1023) / 1024 : 0;
+                    : rows->bits == 6 ? route_block<Id, 6>(mode)
+                                      : route_block<Id, 8>(mode);
+        const int64_t ride = !rows             ? 0
+                             : rows->bits == 8 ? (rows->T + 3) / 4
+                                               : (rows->T * rows->KS * 2 + 1023) / 1024;
         const unsigned grid = (unsigned)(nblk + (ride < 2048 ? ride : 2048));
         hipLaunchKernelGGL(kern, dim3(grid), dim3(1024), mode == ROUTE_SELF ? lds_self : lds_block,
                            stream, ids, TK, E, rp.nbits, rp.RC, rp.NB, BM, rb.hist, rb.bad,
@@ -802,7 +814,11 @@ static hipError_t launch_route_t(const Id *ids, int64_t TK, int E, int BM, const
         return hipGetLastError();
     }
     if (rows) {
-        const hipError_t err = launch_mx_quantize_rows(*rows, stream);
+        const hipError_t err =
+            rows->bits == 8 ? launch_i8_quantize_rows(1, rows->x, rows->H, rows->codes,
+                                                      static_cast<float *>(rows->scales), rows->T,
+                                                      rows->H, stream)
+                            : launch_mx_quantize_rows(*rows, stream);
         if (err != hipSuccess)
             return err;
     }
