@@ -431,13 +431,25 @@ int validate_i8_rows(int64_t M, int64_t Kd, int64_t stride, int dtype)
     return MOE_FFN_OK;
 }
 
-// Rows of an M-tile, by the mean rows of a group and the number of 32 x 32 tiles.
+// Rows of an M-tile, by the mean rows of a group and the number of 32 x 32 tiles (whole
+// layers in us, both sides of each rule):
+//  - up to 20 rows: 32, which pads least (64 tokens through 16 experts of 4096 x 1536,
+//    top 4: 71 against 78 with 64);
+//  - up to 1536 tiles: 32, where the waves share a tile's contraction (512 x 1024 x 512,
+//    8 experts, top 2: 32.5 against 39.8 with 128);
+//  - up to 48 rows, most groups fit 64 (512 x 2048 x 1408, 64 experts, top 6: 156 against
+//    159; 128 x 7168 x 2048, 32, top 8: 268 and 300);
+//  - up to 5000 tiles there are too few of 128 (2048 x 1024 x 512, 8 experts, top 2: 45.7
+//    and 50.7);
+//  - else 128 (256 x 4096 x 1536, 16 experts, top 4: 104 against 122 with 64; 768 x 2048 x
+//    1408, 64, top 6: 168 and 188; 4096: 375 and 600).
 int i8_tile_rows(int64_t M, int64_t E, int64_t widest)
 {
     const double rows = (double)M / (double)E;
     const int64_t tiles = moe::max_mtiles_bound(M, (int)E, 32) * ((widest + 31) / 32);
-    return rows <= 20 || tiles <= 1536 ? 32 : rows <= 48 || tiles <= 8192 ? 64 : 128;
+    return rows <= 20 || tiles <= 1536 ? 32 : rows <= 48 || tiles <= 5000 ? 64 : 128;
 }
+bool i8_weights_once(int64_t M, int64_t E) { return M <= 48 * E; }
 
 struct I8ProductLayout {
     int BM;
@@ -695,6 +707,7 @@ int moe_ffn_int8_mm(const moe_ffn_int8_product *p, const void *codes, const floa
     a.KS = d.KS;
     a.panels = w.panels;
     a.BM = L.BM;
+    a.once = i8_weights_once(p->M, w.E);
     // Past what the 256 MB last-level cache holds the output leaves it to the inputs, so
     // that weights that the last call left there are found (24576 x 1408 x 2048 over 64
     // groups: 80 us against 105)
@@ -780,6 +793,7 @@ int moe_ffn_int8_fwd(const moe_ffn_problem *p, const void *x, const void *topk_i
     g.max_mtiles = (int)L.max_mtiles;
     g.E = E;
     g.BM = L.BM;
+    g.once = i8_weights_once(TK, E);
 
     moe::I8GemmArgs g1 = g;
     const moe::I8Dims up(p->H, p->I), down(p->I, p->H);

@@ -45,10 +45,11 @@ __device__ inline uint32_t i8_code_offset(int tile, int KS, int ks)
     return ((uint32_t)tile * (uint32_t)KS + (uint32_t)ks) * 1024u;
 }
 
-// Cache policy of weight loads where a group has one or two M-tiles, so that a
-// weight is read about once: non-temporal, past the token rows that L2 keeps (one
-// token through 8 of 32 experts of 7168 x 2048: 90 us without, 77 with; 128 tokens:
-// 299 and 273; 512 through 64 of 4096 x 1536, top 4: 264 and 247).
+// Cache policy of weight loads where a group has one M-tile or two, so that a weight
+// is read about once: non-temporal, past the token rows that L2 keeps (one token
+// through 8 of 32 experts of 7168 x 2048: 90 us without, 77 with; 128 tokens: 299 and 273;
+// 512 through 64 of 4096 x 1536, top 4: 264 and 247; but 128 rows a group in 64-row
+// tiles, 4096 x 1536: 200 us without, 230 with).
 constexpr int kOnce = 2;
 
 // M-tiles: of the tables, or, without them, of one group of all rows.
@@ -255,7 +256,7 @@ __global__ __launch_bounds__(64 * WV, 8 / WV > 1 ? 8 / WV : 1) void i8_stream_ke
 // straight into registers, since the waves share none; the token rows, which
 // all four waves read, are copied into a ring of LDS stages of two k-steps, 64
 // bytes a row, swizzled so that the 32 rows of a fragment read spread over all banks.
-template <int KIND, int TF>
+template <int KIND, int TF, int POLICY>
 __global__ __launch_bounds__(256, 2) void i8_tile_kernel(I8GemmArgs a)
 {
     using namespace tile;
@@ -346,7 +347,7 @@ __global__ __launch_bounds__(256, 2) void i8_tile_kernel(I8GemmArgs a)
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
                     w.c[j][s] = __builtin_amdgcn_raw_buffer_load_b128(
-                        wc, wl + s * 1024, i8_code_offset(tl[j], a.KS, q), TF == 2 ? kOnce : 0);
+                        wc, wl + s * 1024, i8_code_offset(tl[j], a.KS, q), POLICY);
         };
         i32x16 acc[2][TF];
 #pragma unroll
@@ -505,9 +506,12 @@ static void i8_launch(const I8GemmArgs &a, int num_cus, hipStream_t s)
         else
             run(i8_stream_kernel<KIND, G1 ? 2 : 1, 8, 4>, 1, 512, 2);
     } else if (a.BM == 64) {
-        run(i8_tile_kernel<KIND, 2>, G1 ? 4 : 8, 256, 2);
+        if (a.once)
+            run(i8_tile_kernel<KIND, 2, kOnce>, G1 ? 4 : 8, 256, 2);
+        else
+            run(i8_tile_kernel<KIND, 2, 0>, G1 ? 4 : 8, 256, 2);
     } else {
-        run(i8_tile_kernel<KIND, 4>, G1 ? 4 : 8, 256, 2);
+        run(i8_tile_kernel<KIND, 4, 0>, G1 ? 4 : 8, 256, 2);
     }
 }
 

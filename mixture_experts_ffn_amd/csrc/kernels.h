@@ -334,6 +334,7 @@ struct I8GemmArgs {
     int panels;
     int max_mtiles;              // upper bound of the M-tiles
     int BM;                      // rows of an M-tile: 32, 64 or 128
+    bool once;                   // a weight is read about once (64-row tiles)
     bool stream_out;             // the output does not stay in the last-level cache
 };
 // kind: what the epilogue makes of the sums
