@@ -500,7 +500,8 @@ int moe_ffn_mxfp4_fwd(const moe_ffn_problem *p, int32_t act_format, const void *
  * [0, M].
  *
  * Limits: 0 <= M <= 2^30, 1 <= E <= 1024, Kd and N positive multiples of 8,
- * Kd·N < 2^31, x_stride >= Kd and a multiple of 8.  weight, y, dy, dx and dW
+ * Kd·N < 2^31, x_stride >= Kd and a multiple of 8; (M / 32 + E) times the column
+ * blocks of 64 below 2^31.  weight, y, dy, dx and dW
  * are dense; x's rows are x_stride elements apart. */
 typedef struct {
     int64_t M, E, Kd, N;
@@ -510,7 +511,8 @@ typedef struct {
     int32_t transposed;    /* 1: weight is [E, N, Kd] */
 } moe_ffn_grouped;
 
-/* Workspace of either call below.  Pure host function. */
+/* Workspace of either call below; 0 bytes (ws may then be NULL) for F32 with up
+ * to 64 groups.  Pure host function. */
 int moe_ffn_grouped_workspace_size(const moe_ffn_grouped *g, size_t *ws_bytes);
 int moe_ffn_grouped_mm(const moe_ffn_grouped *g, const void *x, const void *weight,
                        const void *offsets, void *y, void *ws, size_t ws_bytes, void *stream);
@@ -575,14 +577,15 @@ int moe_ffn_int8_quantize_rows(const moe_ffn_int8_rows *r, const void *x, void *
  * of group e (rows of no group: zeros), [M, N] in out_dtype; the sum is exact.
  * offsets [E + 1] as above, or NULL with E = 1: every row.  The weight's dtype
  * is not read.  Limits: those of the weight; one matrix's packed weights below
- * 4 GiB; 0 <= M <= 2^30. */
+ * 4 GiB; M as for the grouped products. */
 typedef struct {
     moe_ffn_int8_weight weight;
     int64_t M;
     int32_t offsets_dtype; /* MOE_FFN_I32 or MOE_FFN_I64 */
     int32_t out_dtype;     /* MOE_FFN_F32 or MOE_FFN_BF16 */
 } moe_ffn_int8_product;
-/* Workspace.  Pure host function. */
+/* Workspace; 0 bytes (ws may then be NULL) with up to 64 groups.  Pure host
+ * function. */
 int moe_ffn_int8_mm_workspace_size(const moe_ffn_int8_product *p, size_t *ws_bytes);
 int moe_ffn_int8_mm(const moe_ffn_int8_product *p, const void *codes, const float *scales,
                     const void *packed, size_t packed_bytes, const void *offsets, void *y,

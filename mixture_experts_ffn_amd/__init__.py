@@ -880,13 +880,18 @@ def _require_offsets(offsets, E):
 
 
 def _workspace(ws, size, device, *args):
-    """The caller's workspace, or one of ``size(*args)`` bytes."""
+    """(tensor, address, bytes) of the caller's workspace, or of one of ``size(*args)`` bytes; the
+    tensor must outlive the call."""
     if ws is None:
-        return torch.empty(size(*args), dtype=torch.uint8, device=device)
-    _require_gpu(ws)
-    if ws.device != device:
-        raise MoEFFNError(1, f"the workspace is on {ws.device}, the call on {device}")
-    return ws
+        n = size(*args)
+        if n == 0:
+            return None, None, 0
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+    else:
+        _require_gpu(ws)
+        if ws.device != device:
+            raise MoEFFNError(1, f"the workspace is on {ws.device}, the call on {device}")
+    return ws, ws.data_ptr(), ws.nbytes
 
 
 def _grouped(x, weight, offsets, transposed) -> Grouped:
@@ -925,7 +930,7 @@ def moe_ffn_grouped_mm_fwd(x, weight, offsets, *, transposed: bool = False, ws=N
     ws = _workspace(ws, grouped_workspace_size, dev, g)
     y = torch.empty((g.M, g.N), dtype=x.dtype, device=dev)
     _launch(lib.moe_ffn_grouped_mm, dev, g, x.data_ptr(), weight.data_ptr(), offsets.data_ptr(),
-            y.data_ptr(), ws.data_ptr(), ws.nbytes)
+            y.data_ptr(), ws[1], ws[2])
     return y
 
 
@@ -945,7 +950,7 @@ def moe_ffn_grouped_mm_bwd(dy, x, weight, offsets, *, transposed: bool = False,
     dx = torch.empty((g.M, g.Kd), dtype=x.dtype, device=dev) if need_dx else None
     dw = torch.empty_like(weight) if need_dw else None
     _launch(lib.moe_ffn_grouped_mm_bwd, dev, g, dy.data_ptr(), x.data_ptr(), weight.data_ptr(),
-            offsets.data_ptr(), _ptr(dx), _ptr(dw), ws.data_ptr(), ws.nbytes)
+            offsets.data_ptr(), _ptr(dx), _ptr(dw), ws[1], ws[2])
     return dx, dw
 
 
@@ -1067,6 +1072,11 @@ def moe_ffn_int8_dequantize(packed: Int8Weight):
     return w
 
 
+def _row_bytes(Kd: int) -> int:
+    """Bytes of a row's codes (moe_ffn_int8_row_bytes, without a call)."""
+    return -(-Kd // 64) * 64
+
+
 def moe_ffn_int8_quantize_rows(x) -> Int8Rows:
     """Token rows [M, Kd] (float32 or bfloat16; rows may be strided) as int8 with a scale for each
     row: max|x| / 127, codes rounded to nearest even."""
@@ -1074,10 +1084,8 @@ def moe_ffn_int8_quantize_rows(x) -> Int8Rows:
     stride = _require_rows("x", x)
     _no_gradient("the int8 quantisation", x)
     M, Kd = x.shape
-    row = ctypes.c_int64()
-    _check(lib.moe_ffn_int8_row_bytes(Kd, ctypes.byref(row)))
     dev = x.device
-    codes = torch.empty((M, row.value), dtype=torch.int8, device=dev)
+    codes = torch.empty((M, _row_bytes(Kd)), dtype=torch.int8, device=dev)
     scales = torch.empty(M, dtype=torch.float32, device=dev)
     _launch(lib.moe_ffn_int8_quantize_rows, dev, Int8RowsShape(M, Kd, stride, _dtype_code(x)),
             x.data_ptr(), codes.data_ptr(), scales.data_ptr())
@@ -1107,7 +1115,7 @@ def moe_ffn_int8_mm(x, weight: Int8Weight, offsets=None, *, out_dtype=None, ws=N
         raise MoEFFNError(2, f"the rows have {rows.Kd} values, the weight contracts {weight.Kd}")
     M = rows.codes.shape[0]
     if (rows.codes.dtype != torch.int8 or rows.scales.dtype != torch.float32
-            or rows.scales.shape != (M,) or rows.codes.shape[1:] != (-(-rows.Kd // 64) * 64,)):
+            or rows.scales.shape != (M,) or rows.codes.shape[1:] != (_row_bytes(rows.Kd),)):
         raise MoEFFNError(2, "the rows do not hold int8 codes [M, Kd rounded up to 64] and float32 "
                              "scales [M]")
     code = I32 if offsets is None else _require_offsets(offsets, weight.E)
@@ -1117,8 +1125,8 @@ def moe_ffn_int8_mm(x, weight: Int8Weight, offsets=None, *, out_dtype=None, ws=N
     ws = _workspace(ws, int8_mm_workspace_size, dev, p)
     y = torch.empty((M, weight.N), dtype=dtype, device=dev)
     _launch(lib.moe_ffn_int8_mm, dev, p, rows.codes.data_ptr(), rows.scales.data_ptr(),
-            weight.data.data_ptr(), weight.data.nbytes, _ptr(offsets), y.data_ptr(), ws.data_ptr(),
-            ws.nbytes)
+            weight.data.data_ptr(), weight.data.nbytes, _ptr(offsets), y.data_ptr(), ws[1],
+            ws[2])
     return y
 
 

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 
+#include "group_view.h"
 #include "host.h"
 #include "i8.h"
 #include "kernels.h"
@@ -94,15 +95,22 @@ int validate_grouped(const moe_ffn_grouped *g)
     return check_groups(g->M, g->E, g->offsets_dtype, std::max(g->Kd, g->N));
 }
 
+// Whether a call's kernels read the set-up's tables, and so need a workspace.
+bool needs_setup(const moe_ffn_grouped &g)
+{
+    return g.dtype != MOE_FFN_F32 || g.E > moe::kViewGroups;
+}
+
 struct GroupedLayout {
-    GroupLayout groups;
+    GroupLayout groups{};
     size_t total;
 };
 GroupedLayout grouped_layout(const moe_ffn_grouped &g)
 {
     GroupedLayout L;
     Taker take;
-    L.groups.lay(take, g.M, g.E, 64);
+    if (needs_setup(g))
+        L.groups.lay(take, g.M, g.E, 64);
     L.total = take.off;
     return L;
 }
@@ -146,9 +154,10 @@ RowsPlan plan_rows(int dtype, const RowsProduct &p, int64_t E, int num_cus)
     return r;
 }
 
-hipError_t run_rows(int dtype, const RowsProduct &p, const RowsPlan &plan, int64_t E,
+hipError_t run_rows(int dtype, const RowsProduct &p, const RowsPlan &plan, const moe::GroupSource &src,
                     const GroupLayout &G, void *ws, int num_cus, hipStream_t s)
 {
+    const int64_t E = src.E;
     const int32_t *offsets = at<int32_t>(ws, G.offsets), *mtile_off = at<int32_t>(ws, G.mtile_off),
                   *mtile_expert = at<int32_t>(ws, G.mtile_expert);
     if (dtype == MOE_FFN_F32) {
@@ -156,9 +165,12 @@ hipError_t run_rows(int dtype, const RowsProduct &p, const RowsPlan &plan, int64
         a.A = static_cast<const float *>(p.a);
         a.B = static_cast<const float *>(p.w);
         a.C = static_cast<float *>(p.out);
-        a.offsets = offsets;
-        a.mtile_off = mtile_off;
-        a.mtile_expert = mtile_expert;
+        a.src = src;
+        if (E > moe::kViewGroups) {
+            a.offsets = offsets;
+            a.mtile_off = mtile_off;
+            a.mtile_expert = mtile_expert;
+        }
         a.E = (int)E;
         a.N = (int)p.N;
         a.K = (int)p.K;
@@ -251,7 +263,7 @@ int moe_ffn_grouped_mm(const moe_ffn_grouped *g, const void *x, const void *weig
     const GroupedLayout L = grouped_layout(*g);
     if ((rc = check_ptr(x, "x")) || (rc = check_ptr(weight, "weight")) ||
         (rc = check_ptr(offsets, "offsets", g->offsets_dtype == MOE_FFN_I64 ? 8 : 4)) ||
-        (rc = check_ptr(y, "y")) || (rc = check_ptr(ws, "ws")))
+        (rc = check_ptr(y, "y")) || (L.total && (rc = check_ptr(ws, "ws"))))
         return rc;
     if (ws_bytes < L.total)
         return fail(MOE_FFN_ERR_WORKSPACE, "workspace too small: %zu < %zu", ws_bytes, L.total);
@@ -265,8 +277,10 @@ int moe_ffn_grouped_mm(const moe_ffn_grouped *g, const void *x, const void *weig
     set_plan(set, plan, L.groups, ws);
     set.out = y;
     set.out_row = g->N * (int64_t)elem_size(g->dtype);
-    HIP_TRY(moe::launch_group_setup(set, s), "group set-up launch");
-    HIP_TRY(run_rows(g->dtype, p, plan, g->E, L.groups, ws, num_cus, s), "grouped product launch");
+    const moe::GroupSource src{offsets, set.off64, g->M, set.E};
+    if (needs_setup(*g))
+        HIP_TRY(moe::launch_group_setup(set, s), "group set-up launch");
+    HIP_TRY(run_rows(g->dtype, p, plan, src, L.groups, ws, num_cus, s), "grouped product launch");
     return MOE_FFN_OK;
 }
 
@@ -285,7 +299,7 @@ int moe_ffn_grouped_mm_bwd(const moe_ffn_grouped *g, const void *dy, const void 
     if (g->M > 0) {
         if ((rc = check_ptr(dy, "dy")) ||
             (rc = check_ptr(offsets, "offsets", g->offsets_dtype == MOE_FFN_I64 ? 8 : 4)) ||
-            (rc = check_ptr(ws, "ws")) || (dx && ((rc = check_ptr(dx, "dx")) ||
+            (L.total && (rc = check_ptr(ws, "ws"))) || (dx && ((rc = check_ptr(dx, "dx")) ||
                                                   (rc = check_ptr(weight, "weight")))) ||
             (d_weight && (rc = check_ptr(x, "x"))))
             return rc;
@@ -317,9 +331,11 @@ int moe_ffn_grouped_mm_bwd(const moe_ffn_grouped *g, const void *dy, const void 
     const int64_t lda = g->transposed ? g->N : g->x_stride, ldb = g->transposed ? g->x_stride : g->N;
     if (d_weight && g->dtype == MOE_FFN_BF16)
         set.order = at<int32_t>(ws, L.groups.order);
-    HIP_TRY(moe::launch_group_setup(set, s), "group set-up launch");
+    const moe::GroupSource src{offsets, set.off64, g->M, set.E};
+    if (needs_setup(*g))
+        HIP_TRY(moe::launch_group_setup(set, s), "group set-up launch");
     if (dx)
-        HIP_TRY(run_rows(g->dtype, p, plan, g->E, L.groups, ws, num_cus, s), "input gradient launch");
+        HIP_TRY(run_rows(g->dtype, p, plan, src, L.groups, ws, num_cus, s), "input gradient launch");
     if (!d_weight)
         return MOE_FFN_OK;
     const int32_t *o = at<int32_t>(ws, L.groups.offsets);
@@ -328,7 +344,8 @@ int moe_ffn_grouped_mm_bwd(const moe_ffn_grouped *g, const void *dy, const void 
         w.A = static_cast<const float *>(a);
         w.B = static_cast<const float *>(b);
         w.C = static_cast<float *>(d_weight);
-        w.offsets = o;
+        w.src = src;
+        w.offsets = needs_setup(*g) ? o : nullptr;
         w.E = (int)g->E;
         w.M = wm;
         w.N = wn;
@@ -453,7 +470,7 @@ bool i8_weights_once(int64_t M, int64_t E) { return M <= 48 * E; }
 
 struct I8ProductLayout {
     int BM;
-    GroupLayout groups;
+    GroupLayout groups{}; // more groups than a wave's lanes
     size_t total;
 };
 I8ProductLayout i8_product_layout(const moe_ffn_int8_product &p)
@@ -461,7 +478,8 @@ I8ProductLayout i8_product_layout(const moe_ffn_int8_product &p)
     I8ProductLayout L;
     L.BM = i8_tile_rows(p.M, p.weight.E, p.weight.N);
     Taker take;
-    L.groups.lay(take, p.M, p.weight.E, L.BM);
+    if (p.weight.E > moe::kViewGroups)
+        L.groups.lay(take, p.M, p.weight.E, L.BM);
     L.total = take.off;
     return L;
 }
@@ -671,7 +689,7 @@ int moe_ffn_int8_mm(const moe_ffn_int8_product *p, const void *codes, const floa
     if ((rc = check_ptr(codes, "codes")) || (rc = check_ptr(scales, "scales", 4)) ||
         (rc = check_packed(&p->weight, packed, packed_bytes)) ||
         (offsets && (rc = check_ptr(offsets, "offsets", p->offsets_dtype == MOE_FFN_I64 ? 8 : 4))) ||
-        (rc = check_ptr(y, "y")) || (rc = check_ptr(ws, "ws")))
+        (rc = check_ptr(y, "y")) || (L.total && (rc = check_ptr(ws, "ws"))))
         return rc;
     if (ws_bytes < L.total)
         return fail(MOE_FFN_ERR_WORKSPACE, "workspace too small: %zu < %zu", ws_bytes, L.total);
@@ -682,7 +700,10 @@ int moe_ffn_int8_mm(const moe_ffn_int8_product *p, const void *codes, const floa
     const moe_ffn_int8_weight &w = p->weight;
     const moe::I8Dims d(w.Kd, w.N / w.panels);
     moe::I8GemmArgs a{};
-    if (offsets) {
+    a.src = {offsets, p->offsets_dtype == MOE_FFN_I64, p->M, (int)w.E};
+    // at most BM - 1 rows of padding a group
+    a.max_mtiles = (int)((p->M + std::min(p->M, w.E) * (L.BM - 1)) / L.BM);
+    if (w.E > moe::kViewGroups) {
         moe::GroupSetup set = L.groups.setup(ws, offsets, p->offsets_dtype, p->M, w.E, L.BM);
         set.out = y;
         set.out_row = w.N * (int64_t)elem_size(p->out_dtype);
@@ -690,9 +711,6 @@ int moe_ffn_int8_mm(const moe_ffn_int8_product *p, const void *codes, const floa
         a.offsets = set.out_offsets;
         a.mtile_off = set.mtile_off;
         a.mtile_expert = set.mtile_expert;
-        a.max_mtiles = (int)L.groups.max_mtiles;
-    } else {
-        a.max_mtiles = (int)((p->M + L.BM - 1) / L.BM);
     }
     a.wcodes = static_cast<const uint8_t *>(packed);
     a.wscales = at<float>(const_cast<void *>(packed), i8_weight_layout(w.E, w.Kd, w.N, w.panels).scales);
@@ -702,6 +720,7 @@ int moe_ffn_int8_mm(const moe_ffn_int8_product *p, const void *codes, const floa
     a.M = p->M;
     a.E = (int)w.E;
     a.topk = 1;
+    a.out_bytes = (int)elem_size(p->out_dtype);
     a.N = (int)w.N;
     a.NT = d.NT;
     a.KS = d.KS;

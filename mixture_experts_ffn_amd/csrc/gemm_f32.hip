@@ -16,6 +16,7 @@
 #include <type_traits>
 
 #include "common.h"
+#include "group_view.h"
 #include "kernels.h"
 
 namespace moe {
@@ -78,7 +79,16 @@ template <int KIND, int BT> __global__ __launch_bounds__(256) void f32_grouped_k
     const int wk = BT == 64 ? 0 : wave * 8; // 32: this wave's part of a step
     constexpr int KW = BT == 64 ? BK : 8;
     const int ntm = TN ? (a.M + BT - 1) / BT : 0, ntn = (a.N + BT - 1) / BT;
-    const int64_t total = TN ? (int64_t)a.E * ntm * ntn : (int64_t)a.mtile_off[a.E] * MT * ntn;
+    GroupView view;
+    if (!a.offsets) {
+        view = group_view(a.src, kF32Rows);
+        if (!TN)
+            zero_ungrouped(view, a.src.M, a.C, (int64_t)a.N * 4);
+    }
+    auto at = [&](int x, int e) { return __builtin_amdgcn_readlane(x, e); };
+    const int64_t total = TN            ? (int64_t)a.E * ntm * ntn
+                          : a.offsets ? (int64_t)a.mtile_off[a.E] * MT * ntn
+                                      : (int64_t)view.total * MT * ntn;
     for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
         // group-major; inside a group column tiles outer, so that tiles in flight share weights
         int e, r0, rows, K;
@@ -90,15 +100,28 @@ template <int KIND, int BT> __global__ __launch_bounds__(256) void f32_grouped_k
             n0 = local / ntm * BT;
             r0 = local % ntm * BT;
             rows = min(BT, a.M - r0);
-            first = a.offsets[e];
-            K = a.offsets[e + 1] - (int)first;
+            first = a.offsets ? a.offsets[e] : at(view.start, e);
+            K = (a.offsets ? a.offsets[e + 1] : at(view.end, e)) - (int)first;
         } else {
-            e = a.mtile_expert[t / (MT * ntn)];
-            const int mt0 = a.mtile_off[e] * MT, mts = a.mtile_off[e + 1] * MT - mt0;
+            const int m = __builtin_amdgcn_readfirstlane((int)(t / (MT * ntn)));
+            int mt0, mts, end;
+            if (a.offsets) {
+                e = a.mtile_expert[m];
+                mt0 = a.mtile_off[e] * MT;
+                mts = a.mtile_off[e + 1] * MT - mt0;
+                r0 = a.offsets[e];
+                end = a.offsets[e + 1];
+            } else {
+                e = view_group(view, a.E, m);
+                mt0 = at(view.mt0, e) * MT;
+                mts = at(view.tiles, e) * MT;
+                r0 = at(view.start, e);
+                end = at(view.end, e);
+            }
             const int64_t local = t - (int64_t)mt0 * ntn;
             n0 = (int)(local / mts) * BT;
-            r0 = a.offsets[e] + (int)(local % mts) * BT;
-            rows = min(BT, a.offsets[e + 1] - r0);
+            r0 += (int)(local % mts) * BT;
+            rows = min(BT, end - r0);
             first = r0;
             K = a.K;
             if (rows <= 0) // the second half of a group's last M-tile

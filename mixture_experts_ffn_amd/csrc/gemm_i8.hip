@@ -11,6 +11,7 @@
 // All run on the 32 x 32 x 32 matrix instruction with the weights as the first
 // operand (its rows are weight columns) and the token rows as the second: a lane
 // then holds 16 weight columns of one token, in groups of four neighbours.
+#include "group_view.h"
 #include "i8.h"
 #include "kernels.h"
 #include "tile_common.h"
@@ -52,22 +53,42 @@ __device__ inline uint32_t i8_code_offset(int tile, int KS, int ks)
 // tiles, 4096 x 1536: 200 us without, 230 with).
 constexpr int kOnce = 2;
 
-// M-tiles: of the tables, or, without them, of one group of all rows.
+// M-tiles: of the tables, or, without them (up to 64 groups), of the caller's offsets.
+// SwiGLU always has the routing's tables.
 struct I8Tile {
     int e, r0, end, mt0, mts; // group, its first row and end, its first M-tile and their number
 };
-__device__ inline int i8_mtiles(const I8GemmArgs &a)
-{
-    return a.mtile_off ? tile::ldc(a.mtile_off, a.E) : a.max_mtiles;
-}
-__device__ inline I8Tile i8_group(const I8GemmArgs &a, int m)
-{
-    using namespace tile;
-    if (!a.mtile_off)
-        return {0, 0, (int)a.M, 0, a.max_mtiles};
-    const int e = ldc(a.mtile_expert, m), mt0 = ldc(a.mtile_off, e);
-    return {e, ldc(a.offsets, e), ldc(a.offsets, e + 1), mt0, ldc(a.mtile_off, e + 1) - mt0};
-}
+template <bool G1> struct I8Groups {
+    GroupView v;
+    int total;
+    __device__ I8Groups(const I8GemmArgs &a, int rows)
+    {
+        if (G1 || a.mtile_off) {
+            total = tile::ldc(a.mtile_off, a.E);
+            return;
+        }
+        if (!a.src.offsets) { // one group of all rows
+            total = (int)((a.src.M + rows - 1) / rows);
+            return;
+        }
+        v = group_view(a.src, rows);
+        total = v.total;
+        zero_ungrouped(v, a.src.M, a.out, (int64_t)a.N * a.out_bytes);
+    }
+    __device__ I8Tile of(const I8GemmArgs &a, int m) const
+    {
+        using namespace tile;
+        if (G1 || a.mtile_off) {
+            const int e = ldc(a.mtile_expert, m), mt0 = ldc(a.mtile_off, e);
+            return {e, ldc(a.offsets, e), ldc(a.offsets, e + 1), mt0, ldc(a.mtile_off, e + 1) - mt0};
+        }
+        if (!a.src.offsets)
+            return {0, 0, (int)a.src.M, 0, total};
+        const int e = view_group(v, a.src.E, uni(m));
+        auto at = [&](int x) { return __builtin_amdgcn_readlane(x, e); };
+        return {e, at(v.start), at(v.end), at(v.mt0), at(v.tiles)};
+    }
+};
 
 // Four neighbouring columns of a token from their sums.
 __device__ inline f32x4 i8_scaled(const i32x16 &acc, int q, float row, f32x4 col)
@@ -120,7 +141,8 @@ __global__ __launch_bounds__(64 * WV, 8 / WV > 1 ? 8 / WV : 1) void i8_stream_ke
     constexpr int PER = G1 ? CT / 2 : CT; // column tiles of a panel
     const int ntt = G1 ? a.NT : a.NT * a.panels;
     const int ncg = (ntt + PER - 1) / PER;
-    const int64_t total = (int64_t)i8_mtiles(a) * ncg;
+    const I8Groups<G1> groups(a, 32);
+    const int64_t total = (int64_t)groups.total * ncg;
     // an XCD's workgroups (blockIdx % 8) take a contiguous part of the tiles, so
     // a group's token rows stay in one L2
     const int xcd = blockIdx.x & 7;
@@ -143,7 +165,7 @@ __global__ __launch_bounds__(64 * WV, 8 / WV > 1 ? 8 / WV : 1) void i8_stream_ke
     auto place = [&](int64_t t, Place &q) {
         const int m = (int)(t / ncg);
         q.cg = uni((int)(t - (int64_t)m * ncg));
-        const I8Tile g = i8_group(a, m);
+        const I8Tile g = groups.of(a, m);
         q.e = g.e;
         const int r0 = g.r0 + (m - g.mt0) * 32;
         q.nr = min(32, g.end - r0);
@@ -270,7 +292,8 @@ __global__ __launch_bounds__(256, 2) void i8_tile_kernel(I8GemmArgs a)
     const int ntt = G1 ? a.NT : a.NT * a.panels;
     const int ncg = (ntt + PER - 1) / PER;
     const int KP = a.KS >> 1; // stages
-    const int total = uni(i8_mtiles(a)) * ncg; // below 2^31 (checked at launch)
+    const I8Groups<G1> groups(a, ROWS);
+    const int total = uni(groups.total) * ncg; // below 2^31 (checked at launch)
     const int64_t etiles = (int64_t)a.NT * a.panels;
     const int xcd = blockIdx.x & 7;
     const int t1 = (int)((int64_t)total * (xcd + 1) / 8), dt = gridDim.x >> 3;
@@ -284,7 +307,7 @@ __global__ __launch_bounds__(256, 2) void i8_tile_kernel(I8GemmArgs a)
     };
     auto place = [&](int t) {
         Place q;
-        const I8Tile g = i8_group(a, uni((int)((unsigned)t / (unsigned)ncg)));
+        const I8Tile g = groups.of(a, uni((int)((unsigned)t / (unsigned)ncg)));
         q.e = uni(g.e);
         const unsigned local = t - g.mt0 * ncg;
         const int grp = uni(local / (unsigned)(GM * ncg));

@@ -298,11 +298,21 @@ struct GroupSetup {
 };
 hipError_t launch_group_setup(const GroupSetup &g, hipStream_t s);
 
+// A caller's offsets as they are, for kernels that form the groups by themselves
+// (group_view.h: up to 64 groups).
+struct GroupSource {
+    const void *offsets; // [E + 1]; int8 products: null, one group of all M rows
+    bool off64;
+    int64_t M;
+    int E;
+};
+
 // fp32 grouped products (gemm_f32.hip)
 struct F32Grouped {
     const float *A, *B;           // NN: x, W [E, K, N]; NT: x, W [E, N, K]; TN: both by rows
     float *C;
-    const int32_t *offsets, *mtile_off, *mtile_expert;
+    const int32_t *offsets, *mtile_off, *mtile_expert; // null: by the source
+    GroupSource src;
     int E, M, N, K;               // TN: M x N of each gradient; else columns N, contraction K
     int64_t lda, ldb;             // row strides
     int max_mtiles;
@@ -327,11 +337,13 @@ struct I8GemmArgs {
     const float *ascales;
     void *out;                   // act [TK, N] fp32 (SwiGLU), else y [M, N]
     const int32_t *sorted_slot;  // SwiGLU: permuted row -> slot
-    const int32_t *offsets, *mtile_off, *mtile_expert; // null tables: one group of M rows
+    const int32_t *offsets, *mtile_off, *mtile_expert; // null: by the source
+    GroupSource src;
     int64_t M;                   // rows of acodes
     int E, topk, N;              // N: output columns
     int NT, KS;                  // column tiles of a panel, k-steps of 32
     int panels;
+    int out_bytes;               // of an output value
     int max_mtiles;              // upper bound of the M-tiles
     int BM;                      // rows of an M-tile: 32, 64 or 128
     bool once;                   // a weight is read about once (64-row tiles)

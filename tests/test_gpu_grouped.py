@@ -43,7 +43,7 @@ def make(M, Kd, N, E, dtype, transposed, sizes, seed=0, offsets_dtype=torch.int3
 def poisoned(m, x, w, off, transposed):
     Kd, N = (w.shape[2], w.shape[1]) if transposed else w.shape[1:]
     g = m.Grouped(x.shape[0], w.shape[0], Kd, N, Kd, m._dtype_code(x), m._ids_code(off), int(transposed))
-    return torch.full((m.grouped_workspace_size(g),), 0xFF, dtype=torch.uint8, device="cuda")
+    return torch.full((max(m.grouped_workspace_size(g), 16),), 0xFF, dtype=torch.uint8, device="cuda")
 
 
 def check(m, data, dtype, transposed):

@@ -157,7 +157,7 @@ def check(m, x, w, off, out, panels=1, rows=None):
     xr = m.moe_ffn_int8_quantize_rows(x.cuda())
     o = None if off is None else off.cuda()
     p = m.Int8Product(pw._stack(), x.shape[0], m.I32 if off is None else m._ids_code(off), m._dtype_code_of(DT[out]))
-    ws = torch.full((m.int8_mm_workspace_size(p),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = torch.full((max(m.int8_mm_workspace_size(p), 16),), 0xFF, dtype=torch.uint8, device="cuda")
     y = m.moe_ffn_int8_mm(xr, pw, o, out_dtype=DT[out], ws=ws)
     torch.cuda.synchronize()
     assert y.dtype == DT[out] and y.shape == (x.shape[0], w.shape[2])

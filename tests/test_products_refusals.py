@@ -68,6 +68,9 @@ def test_grouped_pointers_and_workspace(lib):
         ctypes.byref(g), vp(x), vp(w), vp(o), vp(y), vp(s), n, None)
     for kw in (dict(x=None), dict(w=None), dict(o=None), dict(y=None), dict(s=None)):
         assert fwd(**kw) == 1
+    # fp32 forms up to 64 groups by itself
+    assert m.grouped_workspace_size(grouped(dtype=m.F32, E=64)) == 0
+    assert fwd(s=None, g=grouped(dtype=m.F32, E=65), n=0) == 1
     for kw in (dict(x=FAKE + 8), dict(w=FAKE + 2), dict(o=FAKE + 2), dict(y=FAKE + 4), dict(s=FAKE + 8),
                dict(o=FAKE + 4, g=grouped(offsets_dtype=m.I64))):
         assert fwd(**kw) == 4
@@ -173,15 +176,18 @@ def test_int8_product_rejects(lib):
     # 8 values of Kd take 64 bytes: 2^26 columns are 4 GiB
     assert mm(product(stack(E=1, Kd=8, N=1 << 26))) == 2
     assert mm(product(stack(E=1, Kd=8, N=1 << 20), M=1 << 30)) == 2  # tiles
-    assert mm(c=None) == 1 and mm(s=None) == 1 and mm(w=None) == 1 and mm(y=None) == 1 and mm(ws=None) == 1
+    assert mm(c=None) == 1 and mm(s=None) == 1 and mm(w=None) == 1 and mm(y=None) == 1
     assert mm(o=None) == 1  # four matrices need offsets
     assert mm(c=FAKE + 8) == 4 and mm(s=FAKE + 2) == 4 and mm(w=FAKE + 8) == 4 and mm(o=FAKE + 2) == 4
-    assert mm(y=FAKE + 8) == 4 and mm(ws=FAKE + 8) == 4
+    assert mm(y=FAKE + 8) == 4
     assert mm(product(offsets_dtype=m.I64), o=FAKE + 4) == 4
-    p = product()
+    p = product(stack(E=65))
     assert lib.moe_ffn_int8_mm_workspace_size(ctypes.byref(p), ctypes.byref(n)) == 0
-    assert mm(wsn=n.value - 1) == 5
-    assert lib.moe_ffn_int8_weight_size(ctypes.byref(p.weight), ctypes.byref(n)) == 0
+    assert mm(p, wsn=n.value - 1) == 5 and mm(p, ws=None) == 1 and mm(p, ws=FAKE + 8) == 4
+    p = product(stack(E=64))
+    assert lib.moe_ffn_int8_mm_workspace_size(ctypes.byref(p), ctypes.byref(n)) == 0
+    assert n.value == 0  # up to 64 groups are formed by the product itself
+    assert lib.moe_ffn_int8_weight_size(ctypes.byref(product().weight), ctypes.byref(n)) == 0
     assert mm(wn=n.value - 1) == 5
     assert mm(product(M=0), c=None, s=None, w=None, y=None, ws=None) == 0
 
