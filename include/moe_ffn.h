@@ -574,10 +574,11 @@ int moe_ffn_int8_quantize_rows(const moe_ffn_int8_rows *r, const void *x, void *
                                float *scales, void *stream);
 
 /* y[m, n] = (Σ_k codes[m, k] · code_e[k, n]) · scales[m] · scale_e[n] for the rows
- * of group e (rows of no group: zeros), [M, N] in out_dtype; the sum is exact.
+ * of group e (rows of no group: zeros), [M, N] in out_dtype; the sum is exact
+ * (codes and scales as moe_ffn_int8_quantize_rows writes them, codes above -128).
  * offsets [E + 1] as above, or NULL with E = 1: every row.  The weight's dtype
  * is not read.  Limits: those of the weight; one matrix's packed weights below
- * 4 GiB; M as for the grouped products. */
+ * 4 GiB; 0 <= M <= 2^30; (M / 32 + E) times the column blocks of 32 below 2^31. */
 typedef struct {
     moe_ffn_int8_weight weight;
     int64_t M;
@@ -598,7 +599,8 @@ int moe_ffn_int8_mm(const moe_ffn_int8_product *p, const void *codes, const floa
  * BF16 and Is 0; the flags MOE_FFN_CHECK_IDS and MOE_FFN_CHECK_STATUS apply,
  * others are rejected with MOE_FFN_ERR_SHAPE, and so are calls of 2^24 tokens or
  * more, H or I above 131072, and those whose token codes (T · H bytes, H rounded
- * up to 64) or one expert's packed weights reach 4 GiB. */
+ * up to 64) or one expert's packed weights reach 4 GiB, or whose (T · K / 32 + E)
+ * times the column blocks of 32 of H or 2I reach 2^31. */
 int moe_ffn_int8_workspace_size(const moe_ffn_problem *p, uint32_t flags, size_t *ws_bytes);
 int moe_ffn_int8_fwd(const moe_ffn_problem *p, const void *x, const void *topk_ids,
                      const float *topk_weights, const void *up_packed, const void *down_packed,

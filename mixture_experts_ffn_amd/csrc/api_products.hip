@@ -60,7 +60,8 @@ struct GroupLayout {
 
 constexpr int64_t kMaxRows = int64_t(1) << 30; // row and tile numbers stay within int32
 
-int check_groups(int64_t M, int64_t E, int offsets_dtype, int64_t widest)
+// blocks: of columns, `width` (32 or 64) wide, of the kernel that has most
+int check_groups(int64_t M, int64_t E, int offsets_dtype, int64_t blocks, int width)
 {
     if (M < 0 || M > kMaxRows)
         return fail(MOE_FFN_ERR_SHAPE, "M must be in [0, 2^30] (got %lld)", (long long)M);
@@ -68,9 +69,9 @@ int check_groups(int64_t M, int64_t E, int offsets_dtype, int64_t widest)
         return fail(MOE_FFN_ERR_SHAPE, "E must be in [1, 1024] (got %lld)", (long long)E);
     if (offsets_dtype != MOE_FFN_I32 && offsets_dtype != MOE_FFN_I64)
         return fail(MOE_FFN_ERR_DTYPE, "offsets_dtype must be I32 or I64 (got %d)", offsets_dtype);
-    if (moe::max_mtiles_bound(M, (int)E, 32) * ((widest + 63) / 64) >= (int64_t(1) << 31))
-        return fail(MOE_FFN_ERR_SHAPE, "too many output tiles: M / 32 + E times columns / 64 must be "
-                                       "< 2^31");
+    if (moe::max_mtiles_bound(M, (int)E, 32) * blocks >= (int64_t(1) << 31))
+        return fail(MOE_FFN_ERR_SHAPE, "too many output tiles: M / 32 + E times columns / %d must be "
+                                       "< 2^31", width);
     return MOE_FFN_OK;
 }
 
@@ -92,7 +93,7 @@ int validate_grouped(const moe_ffn_grouped *g)
                     (long long)g->x_stride);
     if (g->transposed != 0 && g->transposed != 1)
         return fail(MOE_FFN_ERR_SHAPE, "transposed must be 0 or 1 (got %d)", g->transposed);
-    return check_groups(g->M, g->E, g->offsets_dtype, std::max(g->Kd, g->N));
+    return check_groups(g->M, g->E, g->offsets_dtype, (std::max(g->Kd, g->N) + 63) / 64, 64);
 }
 
 // Whether a call's kernels read the set-up's tables, and so need a workspace.
@@ -495,7 +496,8 @@ int validate_i8_product(const moe_ffn_int8_product *p)
         return fail(MOE_FFN_ERR_DTYPE, "out_dtype must be F32 or BF16 (got %d)", p->out_dtype);
     if ((rc = check_i8_group(p->weight.Kd, p->weight.N, p->weight.panels)))
         return rc;
-    return check_groups(p->M, p->weight.E, p->offsets_dtype, p->weight.N);
+    const moe::I8Dims d(p->weight.Kd, p->weight.N / p->weight.panels);
+    return check_groups(p->M, p->weight.E, p->offsets_dtype, (int64_t)p->weight.panels * d.NT, 32);
 }
 
 struct I8FwdLayout {
@@ -550,7 +552,8 @@ int validate_i8_fwd(const moe_ffn_problem *p, uint32_t flags)
         return fail(MOE_FFN_ERR_SHAPE, "T must be < 2^24 (got %lld)", (long long)p->T);
     if ((rc = check_i8_group(p->H, 2 * p->I, 2)) || (rc = check_i8_group(p->I, p->H, 1)))
         return rc;
-    if ((rc = check_groups(p->T * p->K, p->E, MOE_FFN_I32, std::max(p->H, p->I))))
+    const int64_t blocks = std::max((p->H + 31) / 32, 2 * ((p->I + 31) / 32));
+    if ((rc = check_groups(p->T * p->K, p->E, MOE_FFN_I32, blocks, 32)))
         return rc;
     if (flags & ~(MOE_FFN_CHECK_IDS | MOE_FFN_CHECK_STATUS))
         return fail(MOE_FFN_ERR_SHAPE, "flags: only CHECK_IDS and CHECK_STATUS apply (got 0x%x)", flags);

@@ -176,6 +176,12 @@ def test_int8_product_rejects(lib):
     # 8 values of Kd take 64 bytes: 2^26 columns are 4 GiB
     assert mm(product(stack(E=1, Kd=8, N=1 << 26))) == 2
     assert mm(product(stack(E=1, Kd=8, N=1 << 20), M=1 << 30)) == 2  # tiles
+    # (2^23 + 1) blocks of 32 rows by 2^8 of 32 columns, counted for each panel
+    for p in (product(stack(E=1, Kd=8, N=1 << 13), M=1 << 28), product(stack(E=1, Kd=8, N=1 << 13, panels=2), M=1 << 28),
+              product(stack(E=1, Kd=8, N=16, panels=2), M=(1 << 30))):
+        few = p.weight.N == 16
+        assert lib.moe_ffn_int8_mm_workspace_size(ctypes.byref(p), ctypes.byref(n)) == (0 if few else 2)
+        assert few or mm(p) == 2
     assert mm(c=None) == 1 and mm(s=None) == 1 and mm(w=None) == 1 and mm(y=None) == 1
     assert mm(o=None) == 1  # four matrices need offsets
     assert mm(c=FAKE + 8) == 4 and mm(s=FAKE + 2) == 4 and mm(w=FAKE + 8) == 4 and mm(o=FAKE + 2) == 4
@@ -199,6 +205,7 @@ def problem(**kw):
 @pytest.mark.parametrize("bad,flags,code", [
     (dict(dtype=m.F32), 0, 3), (dict(Is=24), 0, 2), (dict(H=131080, I=8), 0, 2), (dict(H=8, I=131080), 0, 2),
     (dict(T=1 << 24, H=8), 0, 2), (dict(T=1 << 20, H=4096, I=8), 0, 2), (dict(K=33), 0, 2), (dict(), m.PIPELINE, 2),
+    (dict(T=1 << 23, H=128, I=8192, K=32), 0, 2), (dict(T=1 << 23, H=128, I=4096, K=32), 0, 2),
     (dict(), m.BULK, 2), (dict(T=-1), 0, 2)], ids=str)
 def test_int8_forward_rejects(lib, bad, flags, code):
     p, n = problem(**bad), ctypes.c_size_t()
