@@ -83,6 +83,10 @@ SIZES = [
     (64, 264, 200, 1), (65, 136, 264, 1), (127, 128, 256, 1), (129, 256, 128, 1), (255, 264, 8, 2),
     (257, 8, 264, 1), (300, 256, 256, 5), (500, 384, 512, 3), (601, 264, 200, 6), (640, 512, 256, 2),
     (1000, 128, 256, 2), (700, 256, 384, 9), (90, 1032, 520, 5), (200, 64, 48, 300), (1500, 256, 256, 1),
+    # 256-row tiles whose columns end inside one, in one direction or both
+    (900, 160, 264, 2), (1300, 1288, 416, 3), (2100, 288, 2056, 2),
+    # as many groups as a wave has lanes, one less, one more
+    (400, 40, 48, 63), (400, 40, 48, 64), (400, 40, 48, 65),
 ]
 
 
@@ -308,6 +312,49 @@ def test_two_streams(gpu_lib):
             assert all(torch.equal(p, q) for p, q in zip(want, got))
 
 
+@pytest.mark.parametrize("transposed", [False, True], ids=["kn", "nk"])
+@pytest.mark.parametrize("M,Kd,N,E", [(1500, 256, 512, 2), (1500, 288, 264, 1), (300, 256, 512, 2)])
+def test_strided_rows_of_every_height(gpu_lib, M, Kd, N, E, transposed):
+    say(f"[grouped] strided {M}x{Kd}x{N}/{E} transposed={transposed}")
+    x, w, dy, off = (t.cuda() for t in make(M, Kd, N, E, "bf16", transposed, spread(M, E, tail=9)))
+    wide = torch.full((M, Kd + 24), float("nan"), dtype=x.dtype, device="cuda")
+    rows = wide[:, 8:8 + Kd]
+    rows.copy_(x)
+    want = gpu_lib.moe_ffn_grouped_mm_fwd(x, w, off, transposed=transposed)
+    assert torch.equal(gpu_lib.moe_ffn_grouped_mm_fwd(rows, w, off, transposed=transposed), want)
+    for p, q in zip(gpu_lib.moe_ffn_grouped_mm_bwd(dy, x, w, off, transposed=transposed),
+                    gpu_lib.moe_ffn_grouped_mm_bwd(dy, rows, w, off, transposed=transposed)):
+        assert torch.equal(p, q)
+
+
+def test_graph_of_a_long_product(gpu_lib):
+    """The routed rows decide the kernel at each replay."""
+    say("[grouped] long graph")
+    M, Kd, N, E = 16384, 2048, 2048, 8
+    gen = torch.Generator("cuda").manual_seed(1)
+    x = torch.randn(M, Kd, generator=gen, device="cuda").bfloat16()
+    w = torch.randn(E, Kd, N, generator=gen, device="cuda").bfloat16()
+    even = torch.arange(0, M + 1, M // E, device="cuda")
+    off = even.clone()
+    gpu_lib.moe_ffn_grouped_mm_fwd(x, w, off)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = gpu_lib.moe_ffn_grouped_mm_fwd(x, w, off)
+    skewed = torch.tensor([0, 40, 90, 150, 15000, 15200, 15700, 16000, 16384], device="cuda")
+    for o in (even, skewed, skewed - 8, even):
+        off.copy_(o)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, gpu_lib.moe_ffn_grouped_mm_fwd(x, w, o))
+        for e in (0, 3, 7):
+            a, b = int(o[e].clamp(0)), int(o[e + 1])
+            want = x[a:b].double() @ w[e].double()
+            mag = x[a:b].double().abs() @ w[e].double().abs()
+            sums = (Kd + 2) * 2.0 ** -23 * mag
+            assert bool(((out[a:b].double() - want).abs() <= sums + HALF["bf16"] * (want.abs() + sums)).all())
+
+
 def test_tensors_that_are_refused(gpu_lib):
     say("[grouped] refusals")
     x, w, dy, off = (t.cuda() for t in make(16, 32, 48, 2, "bf16", False, (0, np.array([8, 8]))))
@@ -325,6 +372,41 @@ def test_tensors_that_are_refused(gpu_lib):
             gpu_lib.moe_ffn_grouped_mm_bwd(bad, x, w, off)
 
 
+# long products, for which the routed rows decide the kernel: rows split evenly and by Zipf's law,
+# with empty groups and rows of no group
+@pytest.mark.parametrize("transposed", [False, True], ids=["kn", "nk"])
+@pytest.mark.parametrize("routing", ["even", "zipf"])
+@pytest.mark.parametrize("M,Kd,N,E", [(16384, 2048, 2048, 8), (20000, 1056, 3208, 24), (24576, 1408, 2048, 64)])
+def test_long_products(gpu_lib, M, Kd, N, E, routing, transposed):
+    say(f"[grouped] {M}x{Kd}x{N}/{E} {routing} transposed={transposed}")
+    gen = torch.Generator("cuda").manual_seed(3)
+    p = torch.ones(E, device="cuda")
+    if routing == "zipf":
+        rank = torch.randperm(E, generator=gen, device="cuda")
+        p = (1.0 + rank) ** -1.2 * (rank < E - 2)
+    counts = torch.bincount(torch.multinomial(p, M - 500, replacement=True, generator=gen), minlength=E)
+    off = torch.nn.functional.pad(torch.cumsum(counts, 0), (1, 0)) + 123
+    x = torch.randn(M, Kd, generator=gen, device="cuda").bfloat16()
+    w = (torch.randn(*((E, N, Kd) if transposed else (E, Kd, N)), generator=gen, device="cuda") / Kd ** 0.5).bfloat16()
+    y = gpu_lib.moe_ffn_grouped_mm_fwd(x, w, off, transposed=transposed)
+    dx, dw = gpu_lib.moe_ffn_grouped_mm_bwd(y, x, w, off, transposed=transposed)
+
+    def near(got, a, b, terms):
+        want, mag = a @ b, a.abs() @ b.abs()
+        sums = (terms + 2) * 2.0 ** -23 * mag
+        return bool(((got.double() - want).abs() <= sums + HALF["bf16"] * (want.abs() + sums) + 1e-38).all())
+
+    for e, (a, b) in enumerate(ref.groups(off.cpu().numpy(), M)):
+        we = w[e].double().t().contiguous() if transposed else w[e].double()
+        xe, ye = x[a:b].double(), y[a:b].double()
+        assert near(y[a:b], xe, we, Kd), e
+        assert near(dx[a:b], ye, we.t().contiguous(), N), e
+        g = dw[e].t() if transposed else dw[e]
+        assert near(g, xe.t().contiguous(), ye, b - a), e
+    for t in (y, dx):
+        assert not t[:123].any() and not t[M - 377:].any()
+
+
 @pytest.mark.parametrize("transposed", [False, True], ids=["kn", "nk"])
 def test_past_32_bit_offsets(gpu_lib, transposed):
     """Outputs of more than 2^32 bytes: the last rows against the same rows alone."""
@@ -339,8 +421,8 @@ def test_past_32_bit_offsets(gpu_lib, transposed):
                                           torch.tensor([0, 0, 300], dtype=torch.int32, device="cuda"),
                                           transposed=transposed)
     assert torch.equal(y[-300:], last)
-    gx, _ = gpu_lib.moe_ffn_grouped_mm_bwd(y, x, w, off, transposed=transposed, need_dw=False)
-    lx, _ = gpu_lib.moe_ffn_grouped_mm_bwd(last, x[-300:].contiguous(), w,
-                                           torch.tensor([0, 0, 300], dtype=torch.int32, device="cuda"),
-                                           transposed=transposed, need_dw=False)
-    assert torch.equal(gx[-300:], lx)
+    gx, gw = gpu_lib.moe_ffn_grouped_mm_bwd(y, x, w, off, transposed=transposed)
+    lx, lw = gpu_lib.moe_ffn_grouped_mm_bwd(last, x[-300:].contiguous(), w,
+                                            torch.tensor([0, 0, 300], dtype=torch.int32, device="cuda"),
+                                            transposed=transposed)
+    assert torch.equal(gx[-300:], lx) and torch.equal(gw[1], lw[1])

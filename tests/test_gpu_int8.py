@@ -190,6 +190,7 @@ def offsets(M, E, seed=0, empty=(), head=0, tail=0, dtype=torch.int32):
 SIZES = [
     (1, 8, 8, 1), (1, 7168, 136, 1), (2, 40, 24, 3), (31, 264, 200, 1), (32, 64, 64, 1), (33, 72, 40, 1),
     (65, 128, 96, 2), (90, 1032, 520, 5), (300, 512, 256, 8), (601, 264, 200, 6), (50, 64, 48, 300),
+    (400, 40, 48, 63), (400, 40, 48, 64), (400, 40, 48, 65),
 ]
 # more 32-row tiles than the waves that split a contraction are used for: 64- and 128-row tiles
 TALL = [(700, 72, 2600, 1), (1100, 200, 1504, 1), (900, 64, 3200, 2), (2049, 72, 4136, 1), (2300, 136, 4104, 3),
@@ -344,6 +345,15 @@ TALL_LAYERS = [(1050, 520, 72, 2, 2), (900, 72, 1032, 2, 2), (2049, 1032, 40, 1,
 def test_layer_sizes(gpu_lib, shape):
     say(f"[int8] layer {shape}")
     check_layer(gpu_lib, layer(*shape))
+
+
+# slots in one block, in several, counted ahead, and more experts than a block's table holds; token
+# rows longer than the routing launch takes along
+@pytest.mark.parametrize("shape", [(4100, 40, 32, 5, 3), (8200, 72, 24, 9, 5), (650, 64, 32, 1000, 2),
+                                   (9, 64, 32, 1024, 5), (20, 8200, 64, 4, 2), (5, 8192, 40, 3, 1)], ids=str)
+def test_layer_every_way_of_routing(gpu_lib, shape):
+    say(f"[int8] layer {shape}")
+    check_layer(gpu_lib, layer(*shape, seed=9))
 
 
 @pytest.mark.parametrize("routing", ["replace", "one"])
