@@ -96,7 +96,19 @@ int validate_grouped(const moe_ffn_grouped *g)
     return check_groups(g->M, g->E, g->offsets_dtype, (std::max(g->Kd, g->N) + 63) / 64, 64);
 }
 
-// Whether a call's kernels read the set-up's tables, and so need a workspace.
+// At most BM - 1 rows of padding a group.
+int64_t tiles_of(int64_t M, int64_t E, int64_t BM) { return (M + std::min(M, E) * (BM - 1)) / BM; }
+
+// gemm_rows.hip serves products of up to so many tiles of 32 x 256: it reads the weights
+// once for each 32 rows of a group, but cuts a tile's columns and contraction finer,
+// where the kernels of taller tiles leave most CUs without one.  Both sides in us with
+// weights out of memory ([K, N]; [N, K] weights, those kernels in brackets): 1 row of 7168
+// x 4096 30 (79); 24 (85), 128 rows 57 (135); 50 (109), 256 82 (132); 90 (107), 512 158 (131);
+// 167 (105); 8 rows over 8 of 32 groups 88 (117); 108 (122); 4096 x 1536, 16 groups, 256 rows
+// 51 (63); 62 (70), 512 rows 84 (65); 89 (71); 512 x 512 x 2048 over 4 groups 16 (18); 16 (16).
+constexpr int64_t kFewTiles = 160;
+
+// Whether calls of these sizes may read the set-up's tables, and so need a workspace.
 bool needs_setup(const moe_ffn_grouped &g)
 {
     return g.dtype != MOE_FFN_F32 || g.E > moe::kViewGroups;
@@ -111,7 +123,7 @@ GroupedLayout grouped_layout(const moe_ffn_grouped &g)
     GroupedLayout L;
     Taker take;
     if (needs_setup(g))
-        L.groups.lay(take, g.M, g.E, 64);
+        L.groups.lay(take, g.M, g.E, g.M <= 32 * kFewTiles ? 16 : 64);
     L.total = take.off;
     return L;
 }
@@ -125,21 +137,30 @@ struct RowsProduct {
     bool nt;
 };
 
-// The kernels and the tile heights for a product, by the mean rows of a group: up to
-// 64 tiles of 64 rows, up to 256 of 128, from there on by the model in kernels.h: for
+// The kernels and the tile heights for a product: gemm_rows.hip for few tiles (above),
+// with 16 or 32 rows (48 x 2048 x 2816 over 4 groups by 16 rows 16.2 us, by 32 22.8); else by
+// the mean rows of a group: up to 64 tiles of 64 rows, up to 256 of 128, from there on by the model in kernels.h: for
 // what the host knows, routed rows that split evenly, or, where a product is long
 // beside a launch (a skewed routing decides 10 % of it), by the set-up kernel.
 struct RowsPlan {
     int BM;          // rows of an M-tile; both: of the first tables
+    bool few;        // gemm_rows.hip
     bool fast;       // gemm_mfma.hip serves the low tiles
     bool big, both;  // 256-row tiles; either, as the set-up decides
     moe::TileModel model;
+    // the product forms the groups by itself
+    bool alone(int64_t E) const { return few && E <= moe::kViewGroups; }
 };
 RowsPlan plan_rows(int dtype, const RowsProduct &p, int64_t E, int num_cus)
 {
-    RowsPlan r{64, false, false, false, {}};
+    RowsPlan r{64, false, false, false, false, {}};
     if (dtype == MOE_FFN_F32)
         return r; // moe::kF32Rows
+    if (tiles_of(p.M, E, 32) * ((p.N + 255) / 256) <= kFewTiles) {
+        r.few = true;
+        r.BM = p.M <= 16 * E ? 16 : 32;
+        return r;
+    }
     const double rows = (double)p.M / (double)E;
     r.fast = !p.nt && p.lda == p.K && moe::fast_gemm_supported(1, p.N, p.K);
     r.BM = rows <= 64 ? 64 : 128;
@@ -179,6 +200,24 @@ hipError_t run_rows(int dtype, const RowsProduct &p, const RowsPlan &plan, const
         a.ldb = p.nt ? p.K : p.N;
         a.max_mtiles = (int)moe::max_mtiles_bound(p.M, (int)E, moe::kF32Rows);
         return moe::launch_f32_grouped(p.nt ? moe::F32_NT : moe::F32_NN, a, num_cus, s);
+    }
+    if (plan.few) {
+        moe::RowsArgs a{};
+        a.A = static_cast<const moe::bf16_t *>(p.a);
+        a.W = static_cast<const moe::bf16_t *>(p.w);
+        a.C = static_cast<moe::bf16_t *>(p.out);
+        a.src = src;
+        if (E > moe::kViewGroups) {
+            a.offsets = offsets;
+            a.mtile_off = mtile_off;
+            a.mtile_expert = mtile_expert;
+        }
+        a.E = (int)E;
+        a.N = (int)p.N;
+        a.K = (int)p.K;
+        a.lda = p.lda;
+        a.max_mtiles = tiles_of(p.M, E, plan.BM);
+        return moe::launch_rows(p.nt, plan.BM, a, num_cus, s);
     }
     moe::FastFwdArgs f{};
     f.w2 = p.w;
@@ -279,7 +318,7 @@ int moe_ffn_grouped_mm(const moe_ffn_grouped *g, const void *x, const void *weig
     set.out = y;
     set.out_row = g->N * (int64_t)elem_size(g->dtype);
     const moe::GroupSource src{offsets, set.off64, g->M, set.E};
-    if (needs_setup(*g))
+    if (needs_setup(*g) && !plan.alone(g->E))
         HIP_TRY(moe::launch_group_setup(set, s), "group set-up launch");
     HIP_TRY(run_rows(g->dtype, p, plan, src, L.groups, ws, num_cus, s), "grouped product launch");
     return MOE_FFN_OK;
@@ -333,7 +372,7 @@ int moe_ffn_grouped_mm_bwd(const moe_ffn_grouped *g, const void *dy, const void 
     if (d_weight && g->dtype == MOE_FFN_BF16)
         set.order = at<int32_t>(ws, L.groups.order);
     const moe::GroupSource src{offsets, set.off64, g->M, set.E};
-    if (needs_setup(*g))
+    if (needs_setup(*g) && (d_weight || !plan.alone(g->E)))
         HIP_TRY(moe::launch_group_setup(set, s), "group set-up launch");
     if (dx)
         HIP_TRY(run_rows(g->dtype, p, plan, src, L.groups, ws, num_cus, s), "input gradient launch");
@@ -704,8 +743,7 @@ int moe_ffn_int8_mm(const moe_ffn_int8_product *p, const void *codes, const floa
     const moe::I8Dims d(w.Kd, w.N / w.panels);
     moe::I8GemmArgs a{};
     a.src = {offsets, p->offsets_dtype == MOE_FFN_I64, p->M, (int)w.E};
-    // at most BM - 1 rows of padding a group
-    a.max_mtiles = (int)((p->M + std::min(p->M, w.E) * (L.BM - 1)) / L.BM);
+    a.max_mtiles = (int)tiles_of(p->M, w.E, L.BM);
     if (w.E > moe::kViewGroups) {
         moe::GroupSetup set = L.groups.setup(ws, offsets, p->offsets_dtype, p->M, w.E, L.BM);
         set.out = y;

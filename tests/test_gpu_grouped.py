@@ -312,8 +312,57 @@ def test_two_streams(gpu_lib):
             assert all(torch.equal(p, q) for p, q in zip(want, got))
 
 
+# few rows: 16- and 32-row tiles of every width, contractions that end inside a step or leave waves
+# without one, more groups than a wave has lanes
 @pytest.mark.parametrize("transposed", [False, True], ids=["kn", "nk"])
-@pytest.mark.parametrize("M,Kd,N,E", [(1500, 256, 512, 2), (1500, 288, 264, 1), (300, 256, 512, 2)])
+@pytest.mark.parametrize("size", [(1, 8, 24600, 1), (16, 40, 36872, 1), (5, 200, 25000, 2), (17, 8, 30008, 1), (40, 72, 9000, 3),
+                                  (150, 104, 9608, 2), (33, 2056, 72, 1), (7, 4104, 16, 5), (64, 1096, 1544, 3),
+                                  (8, 40, 48, 100), (30, 136, 264, 70), (100, 520, 8, 2)], ids=str)
+def test_few_rows(gpu_lib, size, transposed):
+    M, Kd, N, E = size
+    say(f"[grouped] few rows {size} transposed={transposed}")
+    check(gpu_lib, make(M, Kd, N, E, "bf16", transposed, spread(M, E, head=M // 5, tail=M // 7)), "bf16", transposed)
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["kn", "nk"])
+def test_few_rows_of_a_matrix_of_4_gib(gpu_lib, transposed):
+    M, Kd, N = 3, 65544, 32760
+    say(f"[grouped] {M}x{Kd}x{N} transposed={transposed}")
+    gen = torch.Generator("cuda").manual_seed(5)
+    x = torch.randn(M, Kd, generator=gen, device="cuda").bfloat16()
+    w = torch.randn(*((1, N, Kd) if transposed else (1, Kd, N)), generator=gen, device="cuda", dtype=torch.bfloat16)
+    off = torch.tensor([0, M], device="cuda")
+    y = gpu_lib.moe_ffn_grouped_mm_fwd(x, w, off, transposed=transposed)
+    for c in (slice(0, 8), slice(N - 200, N)):
+        wc = (w[0, c].double().t() if transposed else w[0, :, c].double()).contiguous()
+        want, mag = x.double() @ wc, x.double().abs() @ wc.abs()
+        sums = (Kd + 2) * 2.0 ** -23 * mag
+        assert bool(((y[:, c].double() - want).abs() <= sums + HALF["bf16"] * (want.abs() + sums)).all())
+        # far above what rounding gives, a step left out or taken twice is too
+        assert float((y[:, c].double() - want).abs().max()) < 0.01 * Kd ** 0.5
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["kn", "nk"])
+def test_few_rows_keep_infinities_apart(gpu_lib, transposed):
+    """Values past K, N and a group's rows are not multiplied: what is infinite there stays there."""
+    say(f"[grouped] infinities transposed={transposed}")
+    M, Kd, N, E = 5, 40, 24, 3
+    x, w, dy, off = (t.cuda() for t in make(M, Kd, N, E, "bf16", transposed, (0, np.array([2, 0, 3]))))
+    clean = gpu_lib.moe_ffn_grouped_mm_fwd(x, w, off, transposed=transposed)
+    w2 = w.clone()
+    w2[1] = float("inf")
+    assert torch.equal(gpu_lib.moe_ffn_grouped_mm_fwd(x, w2, off, transposed=transposed), clean)
+    wide = torch.full((M, Kd + 8), float("inf"), dtype=x.dtype, device="cuda")
+    wide[:, :Kd] = x
+    assert torch.equal(gpu_lib.moe_ffn_grouped_mm_fwd(wide[:, :Kd], w, off, transposed=transposed), clean)
+    w3 = w.clone()
+    (w3[0][3] if transposed else w3[0][:, 3]).fill_(float("inf"))
+    y = gpu_lib.moe_ffn_grouped_mm_fwd(x.abs() + 1, w3, off, transposed=transposed)
+    assert bool(torch.isinf(y[:2, 3]).all()) and bool(torch.isfinite(y[2:]).all())
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["kn", "nk"])
+@pytest.mark.parametrize("M,Kd,N,E", [(20, 256, 512, 2), (1500, 256, 512, 2), (1500, 288, 264, 1), (300, 256, 512, 2)])
 def test_strided_rows_of_every_height(gpu_lib, M, Kd, N, E, transposed):
     say(f"[grouped] strided {M}x{Kd}x{N}/{E} transposed={transposed}")
     x, w, dy, off = (t.cuda() for t in make(M, Kd, N, E, "bf16", transposed, spread(M, E, tail=9)))
@@ -425,4 +474,10 @@ def test_past_32_bit_offsets(gpu_lib, transposed):
     lx, lw = gpu_lib.moe_ffn_grouped_mm_bwd(last, x[-300:].contiguous(), w,
                                             torch.tensor([0, 0, 300], dtype=torch.int32, device="cuda"),
                                             transposed=transposed)
-    assert torch.equal(gx[-300:], lx) and torch.equal(gw[1], lw[1])
+    assert torch.equal(gw[1], lw[1])
+    # 300 rows alone take another kernel, which sums in another order: both are near the formula
+    we = (w[1] if transposed else w[1].t()).double()
+    want, mag = last.double() @ we, last.double().abs() @ we.abs()
+    sums = (N + 2) * 2.0 ** -23 * mag
+    for got in (gx[-300:], lx):
+        assert bool(((got.double() - want).abs() <= sums + HALF["bf16"] * (want.abs() + sums)).all())
