@@ -138,10 +138,11 @@ struct RowsProduct {
 };
 
 // The kernels and the tile heights for a product: gemm_rows.hip for few tiles (above),
-// with 16 or 32 rows (48 x 2048 x 2816 over 4 groups by 16 rows 16.2 us, by 32 22.8); else by
-// the mean rows of a group: up to 64 tiles of 64 rows, up to 256 of 128, from there on by the model in kernels.h: for
-// what the host knows, routed rows that split evenly, or, where a product is long
-// beside a launch (a skewed routing decides 10 % of it), by the set-up kernel.
+// with 16 or 32 rows (48 x 2048 x 2816 over 4 groups by 16 rows 16.2 us, by 32 22.8); else
+// by the mean rows of a group: up to 64 tiles of 64 rows, up to 256 of 128, from there on
+// by the model in kernels.h: for what the host knows, routed rows that split evenly, or,
+// where a product is long beside a launch (a skewed routing decides 10 % of it), by the
+// set-up kernel.
 struct RowsPlan {
     int BM;          // rows of an M-tile; both: of the first tables
     bool few;        // gemm_rows.hip

@@ -11,8 +11,10 @@
 // consecutive values of four k rows; an operand that is contiguous along k is turned
 // on the way in.  Two LDS buffers, and the loads of the next two steps in registers,
 // since a step of a lone workgroup is shorter than a load.  Bound by the matrix
-// instruction (256 flops a clock and CU) in large problems, by the length of the chain
-// of steps in small ones.
+// instruction (256 flops a clock and CU) in large problems: 8192 rows of 4096 x 4096 over 8
+// groups 2420 us NN, 2500 NT, 2370 TN (110 to 116 TFLOP/s; a large library product reaches
+// 154); by the length of the chain of steps in small ones: 1202 rows of 264 x 200 over
+// 6 groups 9.2, 8.3 and 9.9 us.
 #include <type_traits>
 
 #include "common.h"

@@ -123,7 +123,9 @@ __device__ inline I8Columns i8_columns(const I8GemmArgs &a, int tile)
 // tiles (SwiGLU: half gate and the same up tiles); the WV waves split the
 // contraction, each streaming its part of the weights from memory straight into
 // registers with the next D - 1 pairs of k-steps in flight, across the end of a tile
-// too, and are summed through LDS at the end.
+// too, and are summed through LDS at the end.  Bound by the weights' bytes and, below 100 MB
+// of them, by the launch and the first loads: with weights out of memory one row of 7168 x
+// 4096 8.8 us (3.3 TB/s), of 4096 x 28672 24.0 (4.9), 32 rows of 1024 x 8192 4.9.
 template <int CT> struct I8Part {
     u32x4 w[CT][2]; // [tile][k-step]
     u32x4 a[2];
@@ -278,6 +280,13 @@ __global__ __launch_bounds__(64 * WV, 8 / WV > 1 ? 8 / WV : 1) void i8_stream_ke
 // straight into registers, since the waves share none; the token rows, which
 // all four waves read, are copied into a ring of LDS stages of two k-steps, 64
 // bytes a row, swizzled so that the 32 rows of a fragment read spread over all banks.
+//
+// Long products are bound by power: 65536 x 7168 x 4096 over 32 groups 1775 us, 2.17 POP/s,
+// matrix cores busy 65 % at 1.4 GHz; 8192^3 457 to 475 us, 2.3 to 2.4 (a library product
+// 2.5).  Short contractions are bound by what a tile has beside its products, first
+// loads and stores: 24576 x 1408 x 2048 over 64 groups 80 to 100 us, cores busy 31 % at 2.2 GHz;
+// of GEMM1 of 4096 x 2048 x 1408, 64 experts, top 6, 199 us, the stores are 22 and cold
+// weights 33, without both 159.
 template <int KIND, int TF, int POLICY>
 __global__ __launch_bounds__(256, 2) void i8_tile_kernel(I8GemmArgs a)
 {

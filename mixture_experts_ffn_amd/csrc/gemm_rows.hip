@@ -64,7 +64,9 @@ template <bool NT, int P, int TF> struct Step {
     }
 };
 
-template <int DW, int PO> __device__ inline void load_dwords(uint32_t (&d)[DW], __amdgpu_buffer_rsrc_t b, uint32_t at)
+// PO: cache policy
+template <int DW, int PO>
+__device__ inline void load_dwords(uint32_t (&d)[DW], __amdgpu_buffer_rsrc_t b, uint32_t at)
 {
     if constexpr (DW == 4) {
         const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, PO);
@@ -151,7 +153,8 @@ __global__ __launch_bounds__(64 * WV, 8 / WV) void rows_kernel(RowsArgs a)
             const uint32_t at = g.at[NT ? i / 2 : 0];
             const uint32_t by = NT ? (uint32_t)p * (KSTEP * 2) + i % 2 * 16
                                    : ((uint32_t)p * 32u + i) * (uint32_t)a.N * 2u;
-            load_dwords<S::DW, NT ? 0 : kOnce>(s.w[i], g.w, in[NT ? i % 2 : 0] && at != kOutside ? at + by : kOutside);
+            load_dwords<S::DW, NT ? 0 : kOnce>(
+                s.w[i], g.w, in[NT ? i % 2 : 0] && at != kOutside ? at + by : kOutside);
         }
 #pragma unroll
         for (int f = 0; f < TF; ++f)
