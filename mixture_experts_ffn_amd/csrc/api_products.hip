@@ -107,6 +107,19 @@ int64_t tiles_of(int64_t M, int64_t E, int64_t BM) { return (M + std::min(M, E) 
 // 167 (105); 8 rows over 8 of 32 groups 88 (117); 108 (122); 4096 x 1536, 16 groups, 256 rows
 // 51 (63); 62 (70), 512 rows 84 (65); 89 (71); 512 x 512 x 2048 over 4 groups 16 (18); 16 (16).
 constexpr int64_t kFewTiles = 160;
+// fp32, where the other kernel (gemm_f32.hip, in brackets) is bound by the length of its
+// chain of steps: up to 16 mean rows a group, or 64 in all, and more than 1 MB of weights. 1
+// row of 4096 x 4096 25 (67); 24 (68), 32 rows 36 (68); 45 (70), 8 rows over 8 of 32 groups of
+// 2048 x 2816 41 (83); 31 (81), 400 of 512 x 4096 over 32 67 (100); 62 (121), but 300 of 2048 x
+// 2048 over 8 74 (69); 78 (67), 1202 of 264 x 200 over 6 20 (9); 10 (8), 16 of 256 x 256 8.7 (6.2);
+// 7.7 (6.3).
+bool few_tiles(int dtype, int64_t M, int64_t E, int64_t K, int64_t N)
+{
+    if (dtype != MOE_FFN_F32)
+        return tiles_of(M, E, 32) * ((N + 255) / 256) <= kFewTiles;
+    return (M <= 16 * E || M <= 64) && std::min(M, E) * K * N > (1 << 18) &&
+           K * N < (int64_t(1) << 30); // a group's weights below 4 GiB
+}
 
 // Whether calls of these sizes may read the set-up's tables, and so need a workspace.
 bool needs_setup(const moe_ffn_grouped &g)
@@ -123,7 +136,7 @@ GroupedLayout grouped_layout(const moe_ffn_grouped &g)
     GroupedLayout L;
     Taker take;
     if (needs_setup(g))
-        L.groups.lay(take, g.M, g.E, g.M <= 32 * kFewTiles ? 16 : 64);
+        L.groups.lay(take, g.M, g.E, few_tiles(g.dtype, g.M, g.E, g.Kd, g.N) || few_tiles(g.dtype, g.M, g.E, g.N, g.Kd) ? 16 : 64);
     L.total = take.off;
     return L;
 }
@@ -155,13 +168,13 @@ struct RowsPlan {
 RowsPlan plan_rows(int dtype, const RowsProduct &p, int64_t E, int num_cus)
 {
     RowsPlan r{64, false, false, false, false, {}};
-    if (dtype == MOE_FFN_F32)
-        return r; // moe::kF32Rows
-    if (tiles_of(p.M, E, 32) * ((p.N + 255) / 256) <= kFewTiles) {
+    if (few_tiles(dtype, p.M, E, p.K, p.N)) {
         r.few = true;
         r.BM = p.M <= 16 * E ? 16 : 32;
         return r;
     }
+    if (dtype == MOE_FFN_F32)
+        return r; // moe::kF32Rows
     const double rows = (double)p.M / (double)E;
     r.fast = !p.nt && p.lda == p.K && moe::fast_gemm_supported(1, p.N, p.K);
     r.BM = rows <= 64 ? 64 : 128;
@@ -183,6 +196,24 @@ hipError_t run_rows(int dtype, const RowsProduct &p, const RowsPlan &plan, const
     const int64_t E = src.E;
     const int32_t *offsets = at<int32_t>(ws, G.offsets), *mtile_off = at<int32_t>(ws, G.mtile_off),
                   *mtile_expert = at<int32_t>(ws, G.mtile_expert);
+    if (plan.few) {
+        moe::RowsArgs a{};
+        a.A = p.a;
+        a.W = p.w;
+        a.C = p.out;
+        a.src = src;
+        if (E > moe::kViewGroups) {
+            a.offsets = offsets;
+            a.mtile_off = mtile_off;
+            a.mtile_expert = mtile_expert;
+        }
+        a.E = (int)E;
+        a.N = (int)p.N;
+        a.K = (int)p.K;
+        a.lda = p.lda;
+        a.max_mtiles = tiles_of(p.M, E, plan.BM);
+        return moe::launch_rows(dtype == MOE_FFN_BF16, p.nt, plan.BM, a, num_cus, s);
+    }
     if (dtype == MOE_FFN_F32) {
         moe::F32Grouped a{};
         a.A = static_cast<const float *>(p.a);
@@ -201,24 +232,6 @@ hipError_t run_rows(int dtype, const RowsProduct &p, const RowsPlan &plan, const
         a.ldb = p.nt ? p.K : p.N;
         a.max_mtiles = (int)moe::max_mtiles_bound(p.M, (int)E, moe::kF32Rows);
         return moe::launch_f32_grouped(p.nt ? moe::F32_NT : moe::F32_NN, a, num_cus, s);
-    }
-    if (plan.few) {
-        moe::RowsArgs a{};
-        a.A = static_cast<const moe::bf16_t *>(p.a);
-        a.W = static_cast<const moe::bf16_t *>(p.w);
-        a.C = static_cast<moe::bf16_t *>(p.out);
-        a.src = src;
-        if (E > moe::kViewGroups) {
-            a.offsets = offsets;
-            a.mtile_off = mtile_off;
-            a.mtile_expert = mtile_expert;
-        }
-        a.E = (int)E;
-        a.N = (int)p.N;
-        a.K = (int)p.K;
-        a.lda = p.lda;
-        a.max_mtiles = tiles_of(p.M, E, plan.BM);
-        return moe::launch_rows(p.nt, plan.BM, a, num_cus, s);
     }
     moe::FastFwdArgs f{};
     f.w2 = p.w;

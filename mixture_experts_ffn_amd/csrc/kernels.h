@@ -321,17 +321,18 @@ enum { F32_NN = 0, F32_NT = 1, F32_TN = 2 };
 constexpr int kF32Rows = 64; // rows of an M-tile
 hipError_t launch_f32_grouped(int kind, const F32Grouped &a, int num_cus, hipStream_t s);
 
-// bf16 grouped products of few rows a group (gemm_rows.hip)
+// grouped products of few rows a group (gemm_rows.hip), an expert's weights below 4 GiB
 struct RowsArgs {
-    const bf16_t *A, *W;          // rows lda apart; W [E, K, N], or [E, N, K] (nt)
-    bf16_t *C;
+    const void *A, *W;            // rows lda apart; W [E, K, N], or [E, N, K] (nt)
+    void *C;
     const int32_t *offsets, *mtile_off, *mtile_expert; // null: by the source
     GroupSource src;
     int E, N, K;
     int64_t lda;
     int64_t max_mtiles;
 };
-hipError_t launch_rows(bool nt, int BM, const RowsArgs &a, int num_cus, hipStream_t s); // BM: 16 or 32
+// dtype: 0 fp32, 1 bf16; BM: 16 or 32
+hipError_t launch_rows(int dtype, bool nt, int BM, const RowsArgs &a, int num_cus, hipStream_t s);
 
 // ---- int8 (layouts: i8.h) ---------------------------------------------------------
 hipError_t launch_i8_quantize_weight(int dtype, const void *w, void *codes, float *scales, int64_t E,

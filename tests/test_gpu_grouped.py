@@ -315,13 +315,15 @@ def test_two_streams(gpu_lib):
 # few rows: 16- and 32-row tiles of every width, contractions that end inside a step or leave waves
 # without one, more groups than a wave has lanes
 @pytest.mark.parametrize("transposed", [False, True], ids=["kn", "nk"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("size", [(1, 8, 24600, 1), (16, 40, 36872, 1), (5, 200, 25000, 2), (17, 8, 30008, 1), (40, 72, 9000, 3),
                                   (150, 104, 9608, 2), (33, 2056, 72, 1), (7, 4104, 16, 5), (64, 1096, 1544, 3),
-                                  (8, 40, 48, 100), (30, 136, 264, 70), (100, 520, 8, 2)], ids=str)
-def test_few_rows(gpu_lib, size, transposed):
+                                  (8, 40, 48, 100), (30, 136, 264, 70), (100, 520, 8, 2),
+                                  (1, 520, 512, 1), (64, 264, 1000, 1), (70, 1032, 520, 5), (600, 72, 136, 66)], ids=str)
+def test_few_rows(gpu_lib, size, dtype, transposed):
     M, Kd, N, E = size
-    say(f"[grouped] few rows {size} transposed={transposed}")
-    check(gpu_lib, make(M, Kd, N, E, "bf16", transposed, spread(M, E, head=M // 5, tail=M // 7)), "bf16", transposed)
+    say(f"[grouped] few rows {size} {dtype} transposed={transposed}")
+    check(gpu_lib, make(M, Kd, N, E, dtype, transposed, spread(M, E, head=M // 5, tail=M // 7)), dtype, transposed)
 
 
 @pytest.mark.parametrize("transposed", [False, True], ids=["kn", "nk"])
@@ -343,11 +345,29 @@ def test_few_rows_of_a_matrix_of_4_gib(gpu_lib, transposed):
 
 
 @pytest.mark.parametrize("transposed", [False, True], ids=["kn", "nk"])
-def test_few_rows_keep_infinities_apart(gpu_lib, transposed):
+@pytest.mark.parametrize("Kd,N", [(32768, 32768), (32760, 32768)], ids=["past 4 GiB", "below"])
+def test_few_rows_of_a_large_matrix_in_fp32(gpu_lib, Kd, N, transposed):
+    M = 3
+    say(f"[grouped] {M}x{Kd}x{N} fp32 transposed={transposed}")
+    gen = torch.Generator("cuda").manual_seed(5)
+    x = torch.randn(M, Kd, generator=gen, device="cuda")
+    w = torch.randn(*((1, N, Kd) if transposed else (1, Kd, N)), generator=gen, device="cuda")
+    y = gpu_lib.moe_ffn_grouped_mm_fwd(x, w, torch.tensor([0, M], device="cuda"), transposed=transposed)
+    for c in (slice(0, 8), slice(N - 200, N)):
+        wc = (w[0, c].double().t() if transposed else w[0, :, c].double()).contiguous()
+        want, mag = x.double() @ wc, x.double().abs() @ wc.abs()
+        sums = (Kd + 2) * 2.0 ** -23 * mag
+        assert bool(((y[:, c].double() - want).abs() <= sums + HALF["f32"] * (want.abs() + sums)).all())
+        assert float((y[:, c].double() - want).abs().max()) < 1e-4 * Kd ** 0.5
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["kn", "nk"])
+@pytest.mark.parametrize("dtype,Kd,N,E", [("bf16", 40, 24, 3), ("f32", 200, 1000, 3)])
+def test_few_rows_keep_infinities_apart(gpu_lib, dtype, Kd, N, E, transposed):
     """Values past K, N and a group's rows are not multiplied: what is infinite there stays there."""
-    say(f"[grouped] infinities transposed={transposed}")
-    M, Kd, N, E = 5, 40, 24, 3
-    x, w, dy, off = (t.cuda() for t in make(M, Kd, N, E, "bf16", transposed, (0, np.array([2, 0, 3]))))
+    say(f"[grouped] infinities {dtype} transposed={transposed}")
+    M = 5
+    x, w, dy, off = (t.cuda() for t in make(M, Kd, N, E, dtype, transposed, (0, np.array([2, 0, 3]))))
     clean = gpu_lib.moe_ffn_grouped_mm_fwd(x, w, off, transposed=transposed)
     w2 = w.clone()
     w2[1] = float("inf")
