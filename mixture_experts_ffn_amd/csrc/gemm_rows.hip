@@ -173,8 +173,7 @@ __global__ __launch_bounds__(64 * WV, 8 / WV) void rows_kernel(RowsArgs a)
         for (int f = 0; f < TF; ++f)
             g.x[f] = static_cast<const T *>(a.A) + (int64_t)(g.r0 + min(f * 16 + fr, g.nr - 1)) * a.lda + KL * q;
     };
-    // step p, zeros where it lies past the wave's part or past K (a multiple of 8, so 8 k
-    // are in or out)
+    // step p, zeros past K (a multiple of 8, so 8 k are in or out)
     auto load = [&](const Place &g, int p, S &s) {
         bool in[NH];
 #pragma unroll

@@ -292,11 +292,13 @@ def test_graph_replays(gpu_lib, dtype):
             assert torch.equal(a, b)
 
 
-def test_two_streams(gpu_lib):
+@pytest.mark.parametrize("one,two", [((900, 512, 256, 5), (700, 264, 520, 9)), ((16000, 512, 512, 7), (57000, 128, 256, 1))],
+                         ids=["short", "long"])
+def test_two_streams(gpu_lib, one, two):
     """Two calls at once, each with its own workspace, give what they give alone."""
-    say("[grouped] two streams")
-    a = [t.cuda() for t in make(900, 512, 256, 5, "bf16", False, spread(900, 5))]
-    b = [t.cuda() for t in make(700, 264, 520, 9, "bf16", True, spread(700, 9), seed=2)]
+    say(f"[grouped] two streams {one} {two}")
+    a = [t.cuda() for t in make(*one, "bf16", False, spread(one[0], one[3]))]
+    b = [t.cuda() for t in make(*two, "bf16", True, spread(two[0], two[3]), seed=2)]
     run = lambda d, tr: (gpu_lib.moe_ffn_grouped_mm_fwd(d[0], d[1], d[3], transposed=tr),
                          *gpu_lib.moe_ffn_grouped_mm_bwd(d[2], d[0], d[1], d[3], transposed=tr))
     alone = run(a, False), run(b, True)
@@ -381,8 +383,23 @@ def test_few_rows_keep_infinities_apart(gpu_lib, dtype, Kd, N, E, transposed):
     assert bool(torch.isinf(y[:2, 3]).all()) and bool(torch.isfinite(y[2:]).all())
 
 
+# more tiles than the kernel for few rows takes: tiles of 64, 128 and 256 rows, whole or not in columns
+# and contraction
+HEIGHTS = [(150, 512, 512, 100), (150, 520, 552, 100), (2600, 512, 512, 20), (2600, 520, 552, 20), (5000, 512, 512, 8),
+           (5000, 544, 552, 8), (57000, 128, 256, 1), (57000, 160, 264, 2), (30000, 128, 512, 3)]
+
+
 @pytest.mark.parametrize("transposed", [False, True], ids=["kn", "nk"])
-@pytest.mark.parametrize("M,Kd,N,E", [(20, 256, 512, 2), (1500, 256, 512, 2), (1500, 288, 264, 1), (300, 256, 512, 2)])
+@pytest.mark.parametrize("size", HEIGHTS, ids=str)
+def test_every_height(gpu_lib, size, transposed):
+    M, Kd, N, E = size
+    say(f"[grouped] height {size} transposed={transposed}")
+    check(gpu_lib, make(M, Kd, N, E, "bf16", transposed, spread(M, E, head=M // 50, tail=M // 40)), "bf16", transposed)
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["kn", "nk"])
+@pytest.mark.parametrize("M,Kd,N,E", [(150, 512, 512, 100), (2600, 512, 512, 20), (5000, 544, 552, 8), (57000, 160, 264, 1),
+                                      (20, 256, 512, 2), (1500, 256, 512, 2), (1500, 288, 264, 1), (300, 256, 512, 2)])
 def test_strided_rows_of_every_height(gpu_lib, M, Kd, N, E, transposed):
     say(f"[grouped] strided {M}x{Kd}x{N}/{E} transposed={transposed}")
     x, w, dy, off = (t.cuda() for t in make(M, Kd, N, E, "bf16", transposed, spread(M, E, tail=9)))
