@@ -595,7 +595,7 @@ int moe_ffn_int8_mm(const moe_ffn_int8_product *p, const void *codes, const floa
 /* moe_ffn_fwd (saved = NULL) on int8 weights: up_packed of {E, H, 2I, 2 panels},
  * down_packed of {E, I, H, 1 panel}.  The token rows, and act = silu(gate) ⊙ up
  * (in fp32), are quantised row by row before their product; an expert's output
- * row is rounded to bf16 before the combine, as in moe_ffn_fwd.  dtype must be
+ * rows stay in fp32 up to the combine's sum, which is rounded once.  dtype must be
  * BF16 and Is 0; the flags MOE_FFN_CHECK_IDS and MOE_FFN_CHECK_STATUS apply,
  * others are rejected with MOE_FFN_ERR_SHAPE, and so are calls of 2^24 tokens or
  * more, H or I above 131072, and those whose token codes (T · H bytes, H rounded

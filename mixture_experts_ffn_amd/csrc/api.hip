@@ -738,8 +738,8 @@ static int fwd_run(const moe_ffn_problem *p, const void *x, const void *topk_ids
     }
 
     record(ev, MOE_FFN_STAGE_COMBINE, true, s);
-    HIP_TRY(moe::launch_combine(p->dtype, at<void>(ws, L.o), rb.slot_pos, topk_weights, y, p->T,
-                                (int)p->H, (int)p->K, rb.offsets, E, S, s),
+    HIP_TRY(moe::launch_combine(p->dtype, p->dtype, at<void>(ws, L.o), rb.slot_pos, topk_weights, y,
+                                p->T, (int)p->H, (int)p->K, rb.offsets, E, S, s),
             "combine launch");
     record(ev, MOE_FFN_STAGE_COMBINE, false, s);
     if (flags & MOE_FFN_CHECK_STATUS) {
@@ -1609,8 +1609,8 @@ int moe_ffn_mxfp4_fwd(const moe_ffn_problem *p, int32_t act_format, const void *
     g2.srow = L.act.scale_row();
     HIP_TRY(moe::launch_mx_gemm(false, bits, g2, num_cus, s), "gemm2 launch");
 
-    HIP_TRY(moe::launch_combine(MOE_FFN_BF16, g.o, rb.slot_pos, topk_weights, y, p->T, (int)p->H,
-                                (int)p->K, rb.offsets, E, 0, s),
+    HIP_TRY(moe::launch_combine(MOE_FFN_BF16, MOE_FFN_BF16, g.o, rb.slot_pos, topk_weights, y, p->T,
+                                (int)p->H, (int)p->K, rb.offsets, E, 0, s),
             "combine launch");
     if (flags & MOE_FFN_CHECK_STATUS) {
         int32_t st = 0;

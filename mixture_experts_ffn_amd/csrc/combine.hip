@@ -12,6 +12,8 @@
 // workgroup owns whole tokens, reads the K rows in k order, accumulates in
 // fp32 and rounds once, so the result is bitwise reproducible.  A slot whose
 // id was out of range (slot_pos = -1) contributes nothing.
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 
@@ -21,12 +23,13 @@ namespace moe {
 // one token's output row; its K source rows are loaded 8 at a time before
 // they are accumulated in k order, so their latencies overlap.  NT: the rows
 // are read with the non-temporal hint (o larger than the last-level cache,
-// where the GEMM that wrote it leaves no useful copy behind).
-template <typename T, bool NT>
+// where the GEMM that wrote it leaves no useful copy behind).  Y: the type of y,
+// which o may be finer than.
+template <typename T, typename Y, bool NT>
 __global__ __launch_bounds__(256) void combine_kernel(const T *__restrict__ o,
                                                       const int32_t *__restrict__ slot_pos,
                                                       const float *__restrict__ gates,
-                                                      T *__restrict__ y, int H, int K,
+                                                      Y *__restrict__ y, int H, int K,
                                                       const int32_t *__restrict__ offsets,
                                                       int Er, int S, int64_t ntok)
 {
@@ -74,12 +77,13 @@ __global__ __launch_bounds__(256) void combine_kernel(const T *__restrict__ o,
                 acc[j] += to_f32<T>(vv[j]);
         }
     }
-    u32x4 out;
-    T *oo = reinterpret_cast<T *>(&out);
+    typedef std::conditional_t<VEC * sizeof(Y) == 16, u32x4, u32x2> Out;
+    Out out;
+    Y *oo = reinterpret_cast<Y *>(&out);
 #pragma unroll
     for (int j = 0; j < VEC; ++j)
-        oo[j] = from_f32<T>(acc[j]);
-    *reinterpret_cast<u32x4 *>(y + t * H + (int64_t)c * VEC) = out;
+        oo[j] = from_f32<Y>(acc[j]);
+    *reinterpret_cast<Out *>(y + t * H + (int64_t)c * VEC) = out;
 }
 
 // Backward combine (issue page, section 2.2 "Combine(dX)"): one workgroup per
@@ -195,30 +199,34 @@ hipError_t launch_zero_fill(void *p, size_t bytes, hipStream_t stream)
     return hipGetLastError();
 }
 
-hipError_t launch_combine(int dtype, const void *o, const int32_t *slot_pos, const float *gates,
-                          void *y, int64_t T, int H, int K, const int32_t *offsets, int Er, int S,
-                          hipStream_t stream)
+template <typename T, typename Y>
+static hipError_t combine_t(const void *o, const int32_t *slot_pos, const float *gates, void *y,
+                            int64_t ntok, int H, int K, const int32_t *offsets, int Er, int S,
+                            hipStream_t stream)
 {
-    if (T <= 0)
-        return hipSuccess;
-    const int vec = dtype == 1 ? 8 : 4;
-    const unsigned cblocks = (unsigned)((H / vec + 255) / 256);
-    const dim3 grid((unsigned)T, cblocks);
+    constexpr int VEC = 16 / (int)sizeof(T);
+    const dim3 grid((unsigned)ntok, (unsigned)((H / VEC + 255) / 256));
     // o of more than 192 MB does not stay in the 256 MB last-level cache
     // behind the GEMM that wrote it: stream it (skewed shape, 939 MB: the
     // combine 216 -> 184 us); smaller o is re-read from that cache, where
     // the hint made it slower (134 MB: 31 -> 37 us)
-    const bool nt = T * (K + S) * (int64_t)H * (dtype == 1 ? 2 : 4) > ((int64_t)192 << 20);
-    if (dtype == 1) {
-        auto k = nt ? combine_kernel<bf16, true> : combine_kernel<bf16, false>;
-        hipLaunchKernelGGL(k, grid, dim3(256), 0, stream, static_cast<const bf16 *>(o), slot_pos,
-                           gates, static_cast<bf16 *>(y), H, K, offsets, Er, S, T);
-    } else {
-        auto k = nt ? combine_kernel<float, true> : combine_kernel<float, false>;
-        hipLaunchKernelGGL(k, grid, dim3(256), 0, stream, static_cast<const float *>(o), slot_pos,
-                           gates, static_cast<float *>(y), H, K, offsets, Er, S, T);
-    }
+    const bool nt = ntok * (K + S) * (int64_t)H * (int64_t)sizeof(T) > ((int64_t)192 << 20);
+    auto k = nt ? combine_kernel<T, Y, true> : combine_kernel<T, Y, false>;
+    hipLaunchKernelGGL(k, grid, dim3(256), 0, stream, static_cast<const T *>(o), slot_pos, gates,
+                       static_cast<Y *>(y), H, K, offsets, Er, S, ntok);
     return hipGetLastError();
+}
+
+hipError_t launch_combine(int o_dtype, int y_dtype, const void *o, const int32_t *slot_pos,
+                          const float *gates, void *y, int64_t T, int H, int K,
+                          const int32_t *offsets, int Er, int S, hipStream_t stream)
+{
+    if (T <= 0)
+        return hipSuccess;
+    auto run = o_dtype == 1   ? combine_t<bf16, bf16>
+               : y_dtype == 1 ? combine_t<float, bf16>
+                              : combine_t<float, float>;
+    return run(o, slot_pos, gates, y, T, H, K, offsets, Er, S, stream);
 }
 
 } // namespace moe

@@ -390,10 +390,11 @@ hipError_t launch_router_bwd(const RouterArgs &a, hipStream_t s);
 
 // ---- combine ---------------------------------------------------------------------
 // y[t] = Σ_k g[t, k] o[slot_pos[tK+k]] + Σ_c o[offsets[Er] + cT + t] (the S
-// shared-expert chunks, gate 1, after the routed terms; S = 0: none)
-hipError_t launch_combine(int dtype, const void *o, const int32_t *slot_pos, const float *gates,
-                          void *y, int64_t T, int H, int K, const int32_t *offsets, int Er, int S,
-                          hipStream_t stream);
+// shared-expert chunks, gate 1, after the routed terms; S = 0: none).  o in the
+// dtype of y, or in fp32
+hipError_t launch_combine(int o_dtype, int y_dtype, const void *o, const int32_t *slot_pos,
+                          const float *gates, void *y, int64_t T, int H, int K,
+                          const int32_t *offsets, int Er, int S, hipStream_t stream);
 // backward combine: dx[t] = Σ_k dxp[slot_pos[tK+k]] + Σ_c dxp[offsets[Er] + cT + t] and
 // d_topk[t, k] = Σ_j dgp[slot_pos[tK+k], j] (0 for a dropped slot)
 // (all zeros when *status has MOE_DEV_BAD_SAVED or MOE_DEV_BAD_WS)

@@ -99,9 +99,8 @@ def int8_ffn(x, ids, gates, up, down):
 
     The tolerance adds up: four half steps of fp32 for h (the sum's conversion, two scales), silu and the
     product (|silu'| <= 1.1; 16 half steps, and |g| of them for the exponential's argument); an act value that
-    these may carry to another code, and the change of its row's scale; four half steps for o, o
-    and y each rounded to bf16 (half a step is 2^-8 of the value), gates and the sum over K in
-    fp32 (2 K half steps).
+    these may carry to another code, and the change of its row's scale; four half steps for o, gates
+    and the sum over K in fp32 (2 K half steps), y rounded to bf16 (half a step is 2^-8 of the value).
     """
     x, gates = np.asarray(x, np.float64), np.asarray(gates, np.float64)
     T, H = x.shape
@@ -128,7 +127,6 @@ def int8_ffn(x, ids, gates, up, down):
             o = (aq @ wd) * sa[:, None] * sd
             do = (off @ np.abs(wd)) * sd
             do = do + 4 * half * (np.abs(o) + do)
-            do = do + 2.0 ** -8 * (np.abs(o) + do)
             w = gates[t, k][:, None]
             np.add.at(y, t, w * o)
             np.add.at(tol, t, np.abs(w) * do)
