@@ -90,13 +90,30 @@ template <bool G1> struct I8Groups {
     }
 };
 
+// sum * row * col stays in range wherever the whole product does.  A sum below 2^31 times a
+// scale from 2^97 on could pass the largest number though the column's scale brings it back, so of a
+// scale from 2^64 on 2^32 come last: what is multiplied until then lies between
+// 2^(32 - 149), so nothing is lost below, and 2^127 times the column's scale.  A small scale needs
+// nothing: an integer times it is a multiple of the scale's own last place.
+struct I8RowScale {
+    float by, last;
+};
+__device__ inline I8RowScale i8_row_scale(float s)
+{
+    const bool large = fabsf(s) >= 0x1p64f;
+    return {large ? s * 0x1p-32f : s, large ? 0x1p32f : 1.f};
+}
+__device__ inline float i8_scaled(int sum, I8RowScale row, float col)
+{
+    return (float)sum * row.by * col * row.last;
+}
 // Four neighbouring columns of a token from their sums.
-__device__ inline f32x4 i8_scaled(const i32x16 &acc, int q, float row, f32x4 col)
+__device__ inline f32x4 i8_scaled(const i32x16 &acc, int q, I8RowScale row, f32x4 col)
 {
     f32x4 v;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        v[i] = (float)acc[4 * q + i] * row * col[i];
+        v[i] = i8_scaled(acc[4 * q + i], row, col[i]);
     return v;
 }
 __device__ inline f32x4 i8_swiglu(f32x4 g, f32x4 u)
@@ -227,7 +244,7 @@ __global__ __launch_bounds__(64 * WV, 8 / WV > 1 ? 8 / WV : 1) void i8_stream_ke
                         load(q, p + d + D, x[d]);
                 }
         const int cg = q.cg, nr = q.nr, row = q.row, e = q.e;
-        const float as = q.as;
+        const I8RowScale as = i8_row_scale(q.as);
         t += gridDim.x >> 3;
         if (t < t1)
             first();
@@ -250,7 +267,7 @@ __global__ __launch_bounds__(64 * WV, 8 / WV > 1 ? 8 / WV : 1) void i8_stream_ke
             f32x4 o;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                o[i] = (float)v[i] * as * cs[i];
+                o[i] = i8_scaled(v[i], as, cs[i]);
             return o;
         };
         for (int it = wave; it < PER * 4; it += WV) {
@@ -447,7 +464,7 @@ __global__ __launch_bounds__(256, 2) void i8_tile_kernel(I8GemmArgs a)
                                                             8 * q + 4 * h);
 #pragma unroll
         for (int f = 0; f < TF; ++f) {
-            const float rs = a.ascales[first + row_of(f * 32 + fr)];
+            const I8RowScale rs = i8_row_scale(a.ascales[first + row_of(f * 32 + fr)]);
             if constexpr (KIND == I8_BF16) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
