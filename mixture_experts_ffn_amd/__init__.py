@@ -335,6 +335,13 @@ def _require_gpu(*ts):
             raise MoEFFNError(4, "all tensors must be contiguous")
 
 
+def _own_gradient(dy):
+    """``dy`` as the library takes it.  Autograd hands out views into larger buffers (the gradient
+    of a concatenation's part), which may be contiguous and yet start anywhere; those are copied."""
+    dy = dy.contiguous()
+    return dy if dy.data_ptr() % 16 == 0 else dy.clone()
+
+
 def make_problem(x, topk_ids, up_proj_weight, down_proj_weight) -> Problem:
     if x.dim() != 2 or topk_ids.dim() != 2 or up_proj_weight.dim() != 3 or down_proj_weight.dim() != 3:
         raise MoEFFNError(2, "expected x [T,H], topk_ids [T,K], up [E,H,2I], down [E,I,H]")
@@ -616,7 +623,7 @@ class MoEFFNFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         x, topk_ids, topk_weights, up, down, saved = ctx.saved_tensors
-        dx, d_up, d_down, d_topk = moe_ffn_bwd(dy.contiguous(), x, topk_ids, topk_weights, up,
+        dx, d_up, d_down, d_topk = moe_ffn_bwd(_own_gradient(dy), x, topk_ids, topk_weights, up,
                                                down, saved)
         return dx, None, d_topk, d_up, d_down
 
@@ -967,7 +974,7 @@ class MoEGroupedMMFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         x, weight, offsets = ctx.saved_tensors
-        dx, dw = moe_ffn_grouped_mm_bwd(dy.contiguous(), x, weight, offsets,
+        dx, dw = moe_ffn_grouped_mm_bwd(_own_gradient(dy), x, weight, offsets,
                                         transposed=ctx.transposed,
                                         need_dx=ctx.needs_input_grad[0],
                                         need_dw=ctx.needs_input_grad[1])
