@@ -103,9 +103,9 @@ int64_t tiles_of(int64_t M, int64_t E, int64_t BM) { return (M + std::min(M, E) 
 // once for each 32 rows of a group, but cuts a tile's columns and contraction finer,
 // where the kernels of taller tiles leave most CUs without one.  Both sides in us with
 // weights out of memory ([K, N]; [N, K] weights, those kernels in brackets): 1 row of 7168
-// x 4096 30 (79); 24 (85), 128 rows 57 (135); 50 (109), 256 82 (132); 90 (107), 512 158 (131);
-// 167 (105); 8 rows over 8 of 32 groups 88 (117); 108 (122); 4096 x 1536, 16 groups, 256 rows
-// 51 (63); 62 (70), 512 rows 84 (65); 89 (71); 512 x 512 x 2048 over 4 groups 16 (18); 16 (16).
+// x 4096 30 (79); 24 (85), 128 rows 47 (134); 50 (110), 256 70 (132); 91 (107), 512 133 (131);
+// 167 (106); 8 rows over 8 of 32 groups 88 (117); 108 (122); 4096 x 1536, 16 groups, 256 rows
+// 51 (63); 62 (70), 512 rows 68 (65); 84 (67); 512 x 512 x 2048 over 4 groups 12.6 (19); 16 (17).
 constexpr int64_t kFewTiles = 160;
 // fp32, where the other kernel (gemm_f32.hip, in brackets) is bound by the length of its
 // chain of steps: up to 16 mean rows a group, or 64 in all, and more than 1 MB of weights. 1
@@ -212,6 +212,7 @@ hipError_t run_rows(int dtype, const RowsProduct &p, const RowsPlan &plan, const
         a.K = (int)p.K;
         a.lda = p.lda;
         a.max_mtiles = tiles_of(p.M, E, plan.BM);
+        a.once = moe::weights_once(p.M, E, plan.BM);
         return moe::launch_rows(dtype == MOE_FFN_BF16, p.nt, plan.BM, a, num_cus, s);
     }
     if (dtype == MOE_FFN_F32) {
@@ -505,22 +506,21 @@ int validate_i8_rows(int64_t M, int64_t Kd, int64_t stride, int dtype)
 // Rows of an M-tile, by the mean rows of a group and the number of 32 x 32 tiles (whole
 // layers in us, both sides of each rule):
 //  - up to 20 rows: 32, which pads least (64 tokens through 16 experts of 4096 x 1536,
-//    top 4: 71 against 78 with 64);
+//    top 4: 76 against 81 with 64);
 //  - up to 1536 tiles: 32, where the waves share a tile's contraction (512 x 1024 x 512,
-//    8 experts, top 2: 32.5 against 39.8 with 128);
-//  - up to 48 rows, most groups fit 64 (512 x 2048 x 1408, 64 experts, top 6: 156 against
-//    159; 128 x 7168 x 2048, 32, top 8: 268 and 300);
-//  - up to 5000 tiles there are too few of 128 (2048 x 1024 x 512, 8 experts, top 2: 45.7
-//    and 50.7);
-//  - else 128 (256 x 4096 x 1536, 16 experts, top 4: 104 against 122 with 64; 768 x 2048 x
-//    1408, 64, top 6: 168 and 188; 4096: 375 and 600).
+//    8 experts, top 2: 34 against 42 with 128);
+//  - up to 48 rows, most groups fit 64 (512 x 2048 x 1408, 64 experts, top 6: 153 against
+//    161; 128 x 7168 x 2048, 32, top 8: 267 and 301);
+//  - up to 5000 tiles there are too few of 128 (2048 x 1024 x 512, 8 experts, top 2: 50
+//    and 54);
+//  - else 128 (256 x 4096 x 1536, 16 experts, top 4: 106 against 125 with 64; 768 x 2048 x
+//    1408, 64, top 6: 176 and 197; 4096: 408 and 483).
 int i8_tile_rows(int64_t M, int64_t E, int64_t widest)
 {
     const double rows = (double)M / (double)E;
     const int64_t tiles = moe::max_mtiles_bound(M, (int)E, 32) * ((widest + 31) / 32);
     return rows <= 20 || tiles <= 1536 ? 32 : rows <= 48 || tiles <= 5000 ? 64 : 128;
 }
-bool i8_weights_once(int64_t M, int64_t E) { return M <= 48 * E; }
 
 struct I8ProductLayout {
     int BM;
@@ -781,7 +781,7 @@ int moe_ffn_int8_mm(const moe_ffn_int8_product *p, const void *codes, const floa
     a.KS = d.KS;
     a.panels = w.panels;
     a.BM = L.BM;
-    a.once = i8_weights_once(p->M, w.E);
+    a.once = moe::weights_once(p->M, w.E, L.BM);
     // Past what the 256 MB last-level cache holds the output leaves it to the inputs, so
     // that weights that the last call left there are found (24576 x 1408 x 2048 over 64
     // groups: 80 us against 105)
@@ -867,7 +867,7 @@ int moe_ffn_int8_fwd(const moe_ffn_problem *p, const void *x, const void *topk_i
     g.max_mtiles = (int)L.max_mtiles;
     g.E = E;
     g.BM = L.BM;
-    g.once = i8_weights_once(TK, E);
+    g.once = moe::weights_once(TK, E, L.BM);
 
     moe::I8GemmArgs g1 = g;
     const moe::I8Dims up(p->H, p->I), down(p->I, p->H);

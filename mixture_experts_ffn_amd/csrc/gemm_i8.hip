@@ -46,11 +46,15 @@ __device__ inline uint32_t i8_code_offset(int tile, int KS, int ks)
     return ((uint32_t)tile * (uint32_t)KS + (uint32_t)ks) * 1024u;
 }
 
-// Cache policy of weight loads where a group has one M-tile or two, so that a weight
-// is read about once: non-temporal, past the token rows that L2 keeps (one token
-// through 8 of 32 experts of 7168 x 2048: 90 us without, 77 with; 128 tokens: 299 and 273;
-// 512 through 64 of 4096 x 1536, top 4: 264 and 247; but 128 rows a group in 64-row
-// tiles, 4096 x 1536: 200 us without, 230 with).
+// Cache policy of weight loads where a group mostly has one M-tile (weights_once in
+// kernels.h), so that a weight is read about once: non-temporal, past the token rows that L2
+// keeps (one token through 8 of 32 experts of 7168 x 2048: 90 us without, 77 with; 128 tokens: 299
+// and 273; 512 through 64 of 4096 x 1536, top 4: 264 and 247; but 128 rows a group in 64-row
+// tiles, 4096 x 1536: 200 us without, 230 with).  The streaming kernel, weights out of memory,
+// without and with: 32 rows of 7168 x 4096 15.3 and 14.5, 128 over 16 groups of 4096 x 1536 25.4 and 22.8,
+// 160 over 8 of 2048 x 1408 10.2 and 9.2; more M-tiles a group: 33 rows of 7168 x 4096 13.5 and 15.7, 256
+// over 8 groups of 7168 x 1024 24.8 and 27.4, 600 over 8 of 4096 x 1408 24.4 and 30.8, 1500 rows of 4096 x
+// 1024 22.4 and 35.6.
 constexpr int kOnce = 2;
 
 // M-tiles: of the tables, or, without them (up to 64 groups), of the caller's offsets.
@@ -148,7 +152,7 @@ template <int CT> struct I8Part {
     u32x4 a[2];
 };
 
-template <int KIND, int CT, int WV, int D>
+template <int KIND, int CT, int WV, int D, int POLICY>
 __global__ __launch_bounds__(64 * WV, 8 / WV > 1 ? 8 / WV : 1) void i8_stream_kernel(I8GemmArgs a)
 {
     using namespace tile;
@@ -208,7 +212,7 @@ __global__ __launch_bounds__(64 * WV, 8 / WV > 1 ? 8 / WV : 1) void i8_stream_ke
 #pragma unroll
             for (int j = 0; j < CT; ++j)
                 x.w[j][s] = __builtin_amdgcn_raw_buffer_load_b128(
-                    q.wc, wl + s * 1024, i8_code_offset(q.tile[j], a.KS, p * 2), kOnce);
+                    q.wc, wl + s * 1024, i8_code_offset(q.tile[j], a.KS, p * 2), POLICY);
         }
     };
     int64_t t = total * xcd / 8 + (blockIdx.x >> 3);
@@ -550,10 +554,15 @@ static void i8_launch(const I8GemmArgs &a, int num_cus, hipStream_t s)
     if (a.BM == 32) {
         // tiles of two column tiles by four waves, if there is one for each CU; else a
         // single one (SwiGLU: a pair) by eight
-        if ((int64_t)a.max_mtiles * (G1 ? ntt : (ntt + 1) / 2) >= num_cus)
-            run(i8_stream_kernel<KIND, 2, 4, 4>, G1 ? 1 : 2, 256, 2);
+        const bool two = (int64_t)a.max_mtiles * (G1 ? ntt : (ntt + 1) / 2) >= num_cus;
+        if (two && a.once)
+            run(i8_stream_kernel<KIND, 2, 4, 4, kOnce>, G1 ? 1 : 2, 256, 2);
+        else if (two)
+            run(i8_stream_kernel<KIND, 2, 4, 4, 0>, G1 ? 1 : 2, 256, 2);
+        else if (a.once)
+            run(i8_stream_kernel<KIND, G1 ? 2 : 1, 8, 4, kOnce>, 1, 512, 2);
         else
-            run(i8_stream_kernel<KIND, G1 ? 2 : 1, 8, 4>, 1, 512, 2);
+            run(i8_stream_kernel<KIND, G1 ? 2 : 1, 8, 4, 0>, 1, 512, 2);
     } else if (a.BM == 64) {
         if (a.once)
             run(i8_tile_kernel<KIND, 2, kOnce>, G1 ? 4 : 8, 256, 2);

@@ -38,8 +38,11 @@ namespace rows {
 
 constexpr uint32_t kOutside = 0xFFFFFFF0u; // a buffer offset past any matrix: loads zeros
 __device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0u, 0u, 0u, 0u};
-// [K, N] weights are loaded non-temporally, past the token rows that L2 keeps (8 rows of 7168
-// x 4096 over 8 groups: 89 us against 98 without); of [N, K] weights the two loads that
+// [K, N] weights that are read about once (weights_once in kernels.h) are loaded non-temporally,
+// past the token rows that L2 keeps: 8 rows of 7168 x 4096 over 8 groups 89 us against 98 without,
+// 128 of 4096 x 1536 over 16 42 against 45, fp32 8 of 2048 x 2816 over 32 50 against 54; but with more M-tiles a
+// group, and so more reads of them, 48 rows of 7168 x 4096 46 us against 35.5 without, 512 over 8
+// groups of 7168 x 1024 93.5 against 75, 5000 of 4096 x 256 63 against 38.  Of [N, K] weights the two loads that
 // share a line come apart by it (132 us against 109 without).
 constexpr int kOnce = 2;
 
@@ -109,7 +112,7 @@ __device__ inline void load_dwords(uint32_t (&d)[DW], __amdgpu_buffer_rsrc_t b, 
     }
 }
 
-template <typename T, bool NT, int P, int TF, int WV, int D>
+template <typename T, bool NT, int P, int TF, int WV, int D, int POLICY>
 __global__ __launch_bounds__(64 * WV, 8 / WV) void rows_kernel(RowsArgs a)
 {
     using namespace tile;
@@ -184,7 +187,7 @@ __global__ __launch_bounds__(64 * WV, 8 / WV) void rows_kernel(RowsArgs a)
             const uint32_t at = g.at[NT ? i / 2 : 0];
             const uint32_t by = NT ? (uint32_t)p * (KSTEP * IT) + i % 2 * 16
                                    : ((uint32_t)p * 32u + i) * (uint32_t)a.N * IT;
-            load_dwords<S::DW, NT ? 0 : kOnce>(
+            load_dwords<S::DW, POLICY>(
                 s.w[i], g.w, in[i % NH] && at != kOutside ? at + by : kOutside);
         }
 #pragma unroll
@@ -269,7 +272,11 @@ static hipError_t launch(const RowsArgs &a, int num_cus, hipStream_t s)
     if (most < grid)
         grid = most;
     grid = (grid + 7) / 8 * 8; // a whole number of workgroups for each XCD
-    hipLaunchKernelGGL((rows_kernel<T, NT, P, TF, WV, D>), dim3((unsigned)grid), dim3(64 * WV), 0, s, a);
+    auto k = rows_kernel<T, NT, P, TF, WV, D, 0>;
+    if constexpr (!NT)
+        if (a.once)
+            k = rows_kernel<T, NT, P, TF, WV, D, kOnce>;
+    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(64 * WV), 0, s, a);
     return hipGetLastError();
 }
 

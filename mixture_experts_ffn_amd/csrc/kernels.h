@@ -274,6 +274,16 @@ __host__ __device__ inline bool tall_tiles(const TileModel &m, float rows, float
     return tall < low;
 }
 
+// Whether weights are read about once by M-tiles of BM rows (the policies that follow from it, and
+// both sides of the rule, stand at kOnce in gemm_i8.hip and gemm_rows.hip): M rows over E groups fill
+// three quarters of a tile at the mean, so that a group mostly has one; of 16-row tiles, which are taken
+// up to 16 mean rows, the whole (fp32 400 rows over 32 groups of 512 x 4096 68.5 us with, 74 without; bf16 256
+// of 4096 x 1536 over 16 43 and 46); or all rows lie in one tile.
+inline bool weights_once(int64_t M, int64_t E, int64_t BM)
+{
+    return 4 * M <= 3 * (BM < 32 ? 32 : BM) * E || M <= BM;
+}
+
 // ---- row groups by offsets (group.hip) ---------------------------------------------
 // What the grouped products' kernels read, from a caller's offsets: checked
 // offsets, M-tile tables of BM rows, the groups by descending rows, zeroed
@@ -330,6 +340,7 @@ struct RowsArgs {
     int E, N, K;
     int64_t lda;
     int64_t max_mtiles;
+    bool once;                    // a weight is read about once
 };
 // dtype: 0 fp32, 1 bf16; BM: 16 or 32
 hipError_t launch_rows(int dtype, bool nt, int BM, const RowsArgs &a, int num_cus, hipStream_t s);
@@ -359,7 +370,7 @@ struct I8GemmArgs {
     int out_bytes;               // of an output value
     int max_mtiles;              // upper bound of the M-tiles
     int BM;                      // rows of an M-tile: 32, 64 or 128
-    bool once;                   // a weight is read about once (64-row tiles)
+    bool once;                   // a weight is read about once (tiles of 32 and 64 rows)
     bool stream_out;             // the output does not stay in the last-level cache
 };
 // kind: what the epilogue makes of the sums
