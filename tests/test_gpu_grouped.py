@@ -76,14 +76,14 @@ def spread(M, E, seed=0, empty=(), head=0, tail=0):
     return head, np.bincount(rng.choice(E, n, p=p / p.sum()), minlength=E) if n else np.zeros(E, int)
 
 
-# (M, Kd, N, E): one row, tile edges in rows, columns and contraction, sizes that take the whole-tile
-# kernels (N a multiple of 256 and Kd of 128 in one of the directions) on 64-, 128- and 256-row tiles
+# (M, Kd, N, E): one row, tile edges in rows, columns and contraction.  In bf16 most of them take the
+# kernel for few tiles (taller ones: HEIGHTS below, and test_gpu_grouped_tall.py)
 SIZES = [
     (1, 8, 8, 1), (1, 256, 512, 4), (3, 40, 24, 2), (8, 512, 256, 32), (31, 72, 136, 3), (63, 64, 64, 1),
     (64, 264, 200, 1), (65, 136, 264, 1), (127, 128, 256, 1), (129, 256, 128, 1), (255, 264, 8, 2),
     (257, 8, 264, 1), (300, 256, 256, 5), (500, 384, 512, 3), (601, 264, 200, 6), (640, 512, 256, 2),
     (1000, 128, 256, 2), (700, 256, 384, 9), (90, 1032, 520, 5), (200, 64, 48, 300), (1500, 256, 256, 1),
-    # 256-row tiles whose columns end inside one, in one direction or both
+    # columns that end inside a 256-row tile: of dx and of y in the last two
     (900, 160, 264, 2), (1300, 1288, 416, 3), (2100, 288, 2056, 2),
     # as many groups as a wave has lanes, one less, one more
     (400, 40, 48, 63), (400, 40, 48, 64), (400, 40, 48, 65),

@@ -418,7 +418,7 @@ def test_layer_against_its_parts(gpu_lib):
     act = torch.nn.functional.silu(h[:, :I]) * h[:, I:]
     o = gpu_lib.moe_ffn_int8_mm(act, pd, off, out_dtype=torch.float32)[pos.long()].view(T, K, H)
     want = (torch.from_numpy(gates).cuda().unsqueeze(2) * o).sum(1)
-    # roundings of o and y to bf16, and an act code now and then that moved by one
+    # the rounding of y to bf16, and an act code now and then that moved by one
     assert float((y.float() - want).abs().max() / want.abs().max()) <= 2.0 ** -6
 
 
