@@ -272,10 +272,11 @@ static hipError_t launch(const RowsArgs &a, int num_cus, hipStream_t s)
     if (most < grid)
         grid = most;
     grid = (grid + 7) / 8 * 8; // a whole number of workgroups for each XCD
-    auto k = rows_kernel<T, NT, P, TF, WV, D, 0>;
-    if constexpr (!NT)
-        if (a.once)
-            k = rows_kernel<T, NT, P, TF, WV, D, kOnce>;
+    constexpr int POLICY = NT ? 0 : kOnce; // tiles of 16 rows: always once
+    auto k = rows_kernel<T, NT, P, TF, WV, D, POLICY>;
+    if constexpr (!NT && TF > 1)
+        if (!a.once)
+            k = rows_kernel<T, NT, P, TF, WV, D, 0>;
     hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(64 * WV), 0, s, a);
     return hipGetLastError();
 }

@@ -17,8 +17,6 @@ constexpr int kSetupThreads = 1024;
 
 __device__ inline int32_t held_offset(const GroupSetup &g, int e)
 {
-    if (!g.offsets) // one group of all rows
-        return e == 0 ? 0 : (int32_t)g.M;
     const int64_t v = g.off64 ? static_cast<const int64_t *>(g.offsets)[e]
                               : (int64_t)static_cast<const int32_t *>(g.offsets)[e];
     return (int32_t)(v < 0 ? 0 : v > g.M ? g.M : v);

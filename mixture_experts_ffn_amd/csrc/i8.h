@@ -229,10 +229,4 @@ __device__ inline void i8_quantize_rows(const T *x, int64_t stride, uint8_t *cod
     }
 }
 
-__device__ inline uint32_t i8_pack4(int a, int b, int c, int d)
-{
-    return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 |
-           (uint32_t)d << 24;
-}
-
 } // namespace moe

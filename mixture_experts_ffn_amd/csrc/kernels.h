@@ -289,7 +289,7 @@ inline bool weights_once(int64_t M, int64_t E, int64_t BM)
 // offsets, M-tile tables of BM rows, the groups by descending rows, zeroed
 // tickets; and zeros in the output rows that belong to no group.
 struct GroupSetup {
-    const void *offsets;          // [E + 1]; null: one group of all M rows
+    const void *offsets;          // [E + 1]
     bool off64;
     int64_t M;
     int E, BM;
