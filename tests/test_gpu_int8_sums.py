@@ -71,3 +71,21 @@ def test_slots_that_cancel(gpu_lib, shape):
     # rows rounded to bf16 before the sum would be off by about 2^-9 of each: more than this bound
     one, _ = ref.int8_ffn(as_f64(x), ids[:, :1], gates[:, :1], as_f64(up), as_f64(down))
     assert np.median(tol) < 2.0 ** -10 * np.median(np.abs(one))
+
+
+def test_rows_past_32_bit_offsets(gpu_lib):
+    """Rows of 5.2 GB in all: the last tokens as by themselves, bit for bit (the integer sums are exact
+    and the rest goes in one order, whatever the tiles)."""
+    T, H, I, E, K = 80000, 2048, 32, 8, 8
+    say(f"[int8] layer {T}x{H}x{I}/{E} top {K}")
+    gen = torch.Generator("cuda").manual_seed(6)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    x = r(T, H).bfloat16()
+    up = gpu_lib.moe_ffn_int8_quantize((r(E, H, 2 * I) / H ** 0.5).bfloat16(), panels=2)
+    down = gpu_lib.moe_ffn_int8_quantize((r(E, I, H) / I ** 0.5).bfloat16())
+    ids = torch.rand(T, E, generator=gen, device="cuda").argsort(1).int()
+    gates = torch.rand(T, K, generator=gen, device="cuda")
+    y = gpu_lib.moe_ffn_int8_fwd(x, ids, gates, up, down)
+    for part in (slice(0, 50), slice(T // 2, T // 2 + 700), slice(T - 300, T)):
+        alone = gpu_lib.moe_ffn_int8_fwd(x[part].contiguous(), ids[part].contiguous(), gates[part].contiguous(), up, down)
+        assert torch.equal(y[part], alone) and alone.any()
